@@ -506,6 +506,126 @@ int ulysses_layer_fwd_fused_noalloc(const void* qkv_seq, void* out_seq, int64_t 
                                     const int32_t* cu_seqlens_host, int32_t num_seqs, int32_t* host_status,
                                     void* stream);
 
+/* ---------------------------------------------------------------- 4-bit K/V cache
+ * What decoding needs next to the layer: K and V of the tokens seen so far,
+ * held in 4 bits; attention of one or a few new tokens over them; and a way to
+ * keep the cache within a budget by the attention its tokens received.  The
+ * pages have no counterpart (their layers attend whole sequences); the cast
+ * stands beside the E4M3 cast of ulysses_repack_fwd_fp8.
+ *
+ * A cache holds, for `batch` sequences and `heads` K/V heads, `capacity` slots
+ * each.  It is one device buffer of ulysses_kv4_cache_bytes() (16-byte
+ * aligned, no initial contents needed), three arrays one after another:
+ *
+ *   blocks     [batch, heads, capacity / 32] of 4608 bytes: K codes (32 slots x
+ *              64 bytes), V codes (32 x 64), then 32 x 8 bf16
+ *              ks0, km0, ks1, km1, vs0, vm0, vs1, vm1
+ *   weights    fp32  [batch, heads, capacity] at ulysses_kv4_weight_offset():
+ *              the attention weight each slot has received
+ *   positions  int32 [batch, heads, capacity] at ulysses_kv4_position_offset()
+ *
+ * A row's 128 values are two groups w of 64 (d = 64 w ..), each held as
+ *   x ~ m + s n,  m = min x,  s = bf16((max x - min x) / 15),
+ *   n = round((x - m) / s) in 0..15  (ties to even; 0 where s = 0)
+ * in fp32 arithmetic.  A group that holds an infinity or a NaN, or whose
+ * spread is not finite, is held as s = m = NaN.  Byte 8 g + 4 w + i of a row
+ * holds the code of d = 64 w + 8 g + 2 i in its low half, that of d + 1 in its
+ * high half.
+ *
+ * The number of slots a sequence has filled is the caller's, in device int32
+ * arrays, the same for all its heads; a decoding loop can advance it on the
+ * stream and be captured into a CUDA graph.  A length or slot outside the
+ * cache is not followed (the length is held inside 0..capacity, the row is
+ * skipped) and sets bit 16 of the error word.  Slots at or past a sequence's
+ * length are never read into a result, whatever they hold.  Calls on one
+ * cache are ordered by the caller, as is a workspace that calls share.
+ */
+
+/* ulysses_kv4_attn flags: query i of q_len sees slots below
+ * length - q_len + i + 1 (the last q_len slots are the queries' own tokens)
+ * instead of all; add each slot's attention weight to the cache's weights. */
+#define ULYSSES_KV4_CAUSAL 1u
+#define ULYSSES_KV4_WEIGHTS 2u
+
+typedef struct ulysses_kv4_s ulysses_kv4_t;
+
+/* The geometry of caches (host object, immutable; any number of caches of
+ * this shape).  batch 1..1024, heads 1..1024, batch * heads <= 65535, D = 128,
+ * capacity a multiple of 32.  As ulysses_plan, it holds a 16-byte error word
+ * on the current device, and is created without one where there is none.
+ * Errors: ARG, ALIGN (capacity % 32), UNSUPPORTED. */
+int ulysses_kv4_plan(ulysses_kv4_t** out, int32_t batch, int32_t heads, int32_t D, int64_t capacity);
+void ulysses_kv4_plan_destroy(ulysses_kv4_t* kv);
+size_t ulysses_kv4_cache_bytes(const ulysses_kv4_t* kv);
+size_t ulysses_kv4_weight_offset(const ulysses_kv4_t* kv);
+size_t ulysses_kv4_position_offset(const ulysses_kv4_t* kv);
+
+/*
+ * Quantise `rows` packed bf16 rows of K and V into the cache.  Element d of
+ * row i, head h is at i*token_stride + (h / heads_per_rank)*rank_stride +
+ * (h % heads_per_rank)*head_stride + d: planes of S [n, C, H, D] (heads_per_rank
+ * = heads) and of T [P, C, Np, Hl, D] (heads_per_rank = Hl) alike.  Rows
+ * dev_cu[b] .. dev_cu[b+1]-1 are sequence b's (batch + 1 prefix sums) and go to
+ * slots dev_start[b] on; rows outside are not used.  A new slot's weight is 0,
+ * its position dev_pos0[b] + (row - dev_cu[b]), or its slot if dev_pos0 is NULL.
+ * Strides: multiples of 8 elements, >= 0 (a stride of 0 repeats a row).
+ * Errors: ARG, ALIGN, DIVISIBILITY (heads % heads_per_rank), UNSUPPORTED, CUDA.
+ */
+int ulysses_kv4_append(const ulysses_kv4_t* kv, void* cache, const void* k, const void* v, int64_t rows,
+                       int64_t token_stride, int64_t head_stride, int64_t rank_stride, int32_t heads_per_rank,
+                       const int32_t* dev_cu, const int32_t* dev_start, const int32_t* dev_pos0, void* stream);
+
+/*
+ * The way back: K and V rows as bf16(m + s n), laid out as the append's (for
+ * the attention of a long chunk over its cached prefix by ulysses_attn_fwd).
+ * Rows outside every sequence stay as they are.  Destination rows must not
+ * share elements.  Errors: as ulysses_kv4_append.
+ */
+int ulysses_kv4_load(const ulysses_kv4_t* kv, const void* cache, void* k, void* v, int64_t rows, int64_t token_stride,
+                     int64_t head_stride, int64_t rank_stride, int32_t heads_per_rank, const int32_t* dev_cu,
+                     const int32_t* dev_start, void* stream);
+
+/* Workspace of ulysses_kv4_attn (0 for a shape it refuses): about 10 or 20 MB
+ * of unfinished sums and, with ULYSSES_KV4_WEIGHTS,
+ * 4 * batch * q_heads * q_len * capacity bytes of logits. */
+size_t ulysses_kv4_attn_workspace_bytes(const ulysses_kv4_t* kv, int32_t q_heads, int32_t q_len, uint32_t flags);
+
+/*
+ * out [batch * q_len, q_heads, D] = softmax(softmax_scale * q K^T) V over the
+ * cache's slots below dev_lengths[b] (see ULYSSES_KV4_CAUSAL).  q: bf16, row
+ * b*q_len + i, head h at (b*q_len + i)*q_token_stride + h*q_head_stride; query
+ * heads h*G .. h*G + G-1 share K/V head h (G = q_heads / heads).  lse: NULL, or
+ * fp32 [batch, q_heads, q_len], the base-2 log-sum-exp of the scaled logits. A
+ * row that sees no slot gives zeros and -infinity.  With ULYSSES_KV4_WEIGHTS,
+ * weights[b, h, t] += the sum of slot t's softmax weights over the rows of head
+ * h.  fp32 logits, softmax and sums; weights times scales in fp16 for the second
+ * product.  Meant for few rows (1 to about 16 = G * q_len); more work, each
+ * further 16 reading the cache again.  Errors: ARG, ALIGN, DIVISIBILITY
+ * (q_heads % heads), WORKSPACE, UNSUPPORTED, CUDA.
+ */
+int ulysses_kv4_attn(const ulysses_kv4_t* kv, void* cache, const void* q, int32_t q_heads, int32_t q_len,
+                     int64_t q_token_stride, int64_t q_head_stride, void* out, void* lse, const int32_t* dev_lengths,
+                     float softmax_scale, uint32_t flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Keep at most `keep` slots of every (sequence, head) pair: the first `sink`,
+ * the last `recent` and, of those between, the keep - sink - recent of largest
+ * accumulated weight (of equal weights the lower slots; NaN below every
+ * number).  The kept slots move, in their order, into slots 0 on of the
+ * destination cache (same batch and heads, capacity >= keep) with their
+ * weights and positions; its further slots stay as they are.  A sequence of at
+ * most `keep` slots moves whole.  dev_new_lengths[b] = min(dev_lengths[b],
+ * keep).  The caches must not overlap, nor the two length arrays.
+ * Errors: ARG, ALIGN, CUDA.
+ */
+int ulysses_kv4_evict(const ulysses_kv4_t* src_kv, const void* src_cache, const ulysses_kv4_t* dst_kv, void* dst_cache,
+                      const int32_t* dev_lengths, int32_t* dev_new_lengths, int32_t keep, int32_t sink, int32_t recent,
+                      void* stream);
+
+/* As ulysses_last_device_error: synchronise `stream`, read and clear the
+ * error word (16 = a length, start or slot outside a cache; 1, 4 as there). */
+int ulysses_kv4_last_device_error(const ulysses_kv4_t* kv, void* stream);
+
 /* Static description of a return code. */
 const char* ulysses_strerror(int code);
 

@@ -27,6 +27,8 @@ ULYSSES_ERR_UNSUPPORTED = 8
 ULYSSES_PLAN_CAUSAL = 1
 ULYSSES_PLAN_PAIR_ATTENTION = 2
 ULYSSES_PLAN_DETERMINISTIC = 4
+ULYSSES_KV4_CAUSAL = 1
+ULYSSES_KV4_WEIGHTS = 2
 MAX_SEQS = 64
 MAX_WINDOW_BYTES = 1024 ** 3
 
@@ -41,6 +43,9 @@ EXPORTS = (
     "ulysses_workspace_bytes_fp8", "ulysses_layer_fwd_fp8", "ulysses_repack_fwd_push", "ulysses_attn_fwd_push",
     "ulysses_repack_bwd_push", "ulysses_attn_fwd_lse_slab", "ulysses_attn_bwd_slab", "ulysses_a2a_pack",
     "ulysses_a2a_unpack", "ulysses_layer_fwd_fp8_host",
+    "ulysses_kv4_plan", "ulysses_kv4_plan_destroy", "ulysses_kv4_cache_bytes", "ulysses_kv4_weight_offset",
+    "ulysses_kv4_position_offset", "ulysses_kv4_append", "ulysses_kv4_load", "ulysses_kv4_attn_workspace_bytes",
+    "ulysses_kv4_attn", "ulysses_kv4_evict", "ulysses_kv4_last_device_error",
 )
 
 
@@ -144,6 +149,26 @@ def load() -> ctypes.CDLL:
         lib.ulysses_attn_fwd_lse_slab.restype = ctypes.c_int
         lib.ulysses_attn_bwd_slab.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, ctypes.c_float, vp]
         lib.ulysses_attn_bwd_slab.restype = ctypes.c_int
+        lib.ulysses_kv4_plan.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i64]
+        lib.ulysses_kv4_plan.restype = ctypes.c_int
+        lib.ulysses_kv4_plan_destroy.argtypes = [vp]
+        lib.ulysses_kv4_plan_destroy.restype = None
+        for name in ("ulysses_kv4_cache_bytes", "ulysses_kv4_weight_offset", "ulysses_kv4_position_offset"):
+            getattr(lib, name).argtypes = [vp]
+            getattr(lib, name).restype = sz
+        lib.ulysses_kv4_append.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i32, vp, vp, vp, vp]
+        lib.ulysses_kv4_append.restype = ctypes.c_int
+        lib.ulysses_kv4_load.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i32, vp, vp, vp]
+        lib.ulysses_kv4_load.restype = ctypes.c_int
+        lib.ulysses_kv4_attn_workspace_bytes.argtypes = [vp, i32, i32, ctypes.c_uint32]
+        lib.ulysses_kv4_attn_workspace_bytes.restype = sz
+        lib.ulysses_kv4_attn.argtypes = [vp, vp, vp, i32, i32, i64, i64, vp, vp, vp, ctypes.c_float, ctypes.c_uint32,
+                                         vp, sz, vp]
+        lib.ulysses_kv4_attn.restype = ctypes.c_int
+        lib.ulysses_kv4_evict.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp]
+        lib.ulysses_kv4_evict.restype = ctypes.c_int
+        lib.ulysses_kv4_last_device_error.argtypes = [vp, vp]
+        lib.ulysses_kv4_last_device_error.restype = ctypes.c_int
         _handle = lib
         return lib
 
@@ -463,3 +488,159 @@ def ulysses_layer_fwd_fused_noalloc(qkv_seq, out_seq, N: int, H: int, D: int, P:
         return status.value
     _check(code, "ulysses_layer_fwd_fused_noalloc")
     return status.value
+
+
+# ---------------------------------------------------------------- 4-bit K/V cache
+
+
+class KV4Plan:
+    """Owner of a ulysses_kv4_t*: the geometry of 4-bit K/V caches."""
+
+    def __init__(self, handle: int, batch: int, heads: int, D: int, capacity: int):
+        self._h = ctypes.c_void_p(handle)
+        self.batch, self.heads, self.D, self.capacity = batch, heads, D, capacity
+
+    @property
+    def handle(self) -> ctypes.c_void_p:
+        if not self._h:
+            raise ValueError("plan destroyed")
+        return self._h
+
+    @property
+    def cache_bytes(self) -> int:
+        return load().ulysses_kv4_cache_bytes(self.handle)
+
+    @property
+    def weight_offset(self) -> int:
+        return load().ulysses_kv4_weight_offset(self.handle)
+
+    @property
+    def position_offset(self) -> int:
+        return load().ulysses_kv4_position_offset(self.handle)
+
+    def workspace_bytes(self, q_heads: int, q_len: int, weights: bool = False) -> int:
+        """Workspace of ulysses_kv4_attn."""
+        return load().ulysses_kv4_attn_workspace_bytes(self.handle, int(q_heads), int(q_len),
+                                                       ULYSSES_KV4_WEIGHTS if weights else 0)
+
+    def destroy(self) -> None:
+        if self._h:
+            load().ulysses_kv4_plan_destroy(self._h)
+            self._h = ctypes.c_void_p(None)
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:  # noqa: BLE001 - interpreter shutdown
+            pass
+
+
+def ulysses_kv4_plan(batch: int, heads: int, D: int, capacity: int) -> KV4Plan:
+    """The geometry of 4-bit K/V caches: `capacity` slots (a multiple of 32)
+    for each of `batch` sequences and `heads` K/V heads of D = 128."""
+    h = ctypes.c_void_p()
+    _check(load().ulysses_kv4_plan(ctypes.byref(h), int(batch), int(heads), int(D), int(capacity)),
+           "ulysses_kv4_plan")
+    return KV4Plan(h.value, int(batch), int(heads), int(D), int(capacity))
+
+
+def _kv4_tensor(where: str, name: str, t, dtype: str, numel: int | None = None):
+    """A CUDA tensor of this type (and, where given, a contiguous one of at least numel elements)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != getattr(torch, dtype):
+        raise TypeError(f"{where}: {name} must be a CUDA tensor of type {dtype}")
+    if numel is not None and (not t.is_contiguous() or t.numel() < numel):
+        raise ValueError(f"{where}: {name} must be contiguous with at least {numel} elements")
+    return t
+
+
+def _kv4_rows(where: str, kv: KV4Plan, cache, k, v, cu, start):
+    """The rows argument of append and load: K and V of one shape and layout,
+    [rows, heads, D] or, split over ranks, [P, rows, heads / P, D]."""
+    _kv4_tensor(where, "cache", cache, "uint8", kv.cache_bytes)
+    _kv4_tensor(where, "k", k, "bfloat16")
+    _kv4_tensor(where, "v", v, "bfloat16")
+    _kv4_tensor(where, "cu", cu, "int32", kv.batch + 1)
+    _kv4_tensor(where, "start", start, "int32", kv.batch)
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError(f"{where}: k and v must have one shape and layout")
+    if k.dim() not in (3, 4) or k.shape[-1] != kv.D or (k.numel() and k.stride(-1) != 1):
+        raise ValueError(f"{where}: k and v are [rows, heads, {kv.D}] or [ranks, rows, heads / ranks, {kv.D}]")
+    ranks, (rows, hl) = (k.shape[0] if k.dim() == 4 else 1), k.shape[-3:-1]
+    if ranks * hl != kv.heads:
+        raise ValueError(f"{where}: {ranks * hl} heads, the plan has {kv.heads}")
+    rank_stride = k.stride(0) if k.dim() == 4 else 0
+    return rows, k.stride(-3), k.stride(-2), rank_stride, hl
+
+
+def ulysses_kv4_append(kv: KV4Plan, cache, k, v, cu, start, pos0=None, stream=None) -> None:
+    """Quantise rows of K and V into the cache: rows cu[b] .. cu[b+1]-1 go to
+    slots start[b] on of sequence b.  k, v: bf16 [rows, heads, D] (a plane of
+    packed rows will do) or [P, rows, heads / P, D] (planes of a head slab).
+    pos0: int32 [batch], the position of each sequence's first new row
+    (default: its slot)."""
+    rows, ts, hs, rs, hl = _kv4_rows("ulysses_kv4_append", kv, cache, k, v, cu, start)
+    if pos0 is not None:
+        _kv4_tensor("ulysses_kv4_append", "pos0", pos0, "int32", kv.batch)
+    if rows == 0:
+        return
+    _check(load().ulysses_kv4_append(kv.handle, _ptr(cache), _ptr(k), _ptr(v), rows, ts, hs, rs, hl, _ptr(cu),
+                                     _ptr(start), _ptr(pos0), _stream(stream)), "ulysses_kv4_append")
+
+
+def ulysses_kv4_load(kv: KV4Plan, cache, k, v, cu, start, stream=None) -> None:
+    """Bring slots start[b] on back as bf16 rows cu[b] .. cu[b+1]-1 of k and v
+    (layouts as ulysses_kv4_append)."""
+    rows, ts, hs, rs, hl = _kv4_rows("ulysses_kv4_load", kv, cache, k, v, cu, start)
+    if rows == 0:
+        return
+    _check(load().ulysses_kv4_load(kv.handle, _ptr(cache), _ptr(k), _ptr(v), rows, ts, hs, rs, hl, _ptr(cu),
+                                   _ptr(start), _stream(stream)), "ulysses_kv4_load")
+
+
+def ulysses_kv4_attn(kv: KV4Plan, cache, q, out, lengths, softmax_scale: float, lse=None, causal: bool = False,
+                     weights: bool = False, workspace=None, stream=None) -> None:
+    """Attention of q, bf16 [batch, q_len, q_heads, D] (any strides of rows and
+    heads), over the cache's slots below lengths [batch] (int32) into out, the
+    same shape, contiguous; lse: optional fp32 [batch, q_heads, q_len]."""
+    where = "ulysses_kv4_attn"
+    _kv4_tensor(where, "cache", cache, "uint8", kv.cache_bytes)
+    _kv4_tensor(where, "q", q, "bfloat16")
+    if q.dim() != 4 or q.shape[0] != kv.batch or q.shape[-1] != kv.D or q.stride(-1) != 1:
+        raise ValueError(f"{where}: q is [{kv.batch}, q_len, q_heads, {kv.D}]")
+    B, q_len, q_heads, D = q.shape
+    if q_len > 1 and B > 1 and q.stride(0) != q_len * q.stride(1):
+        raise ValueError(f"{where}: the rows of q must be evenly spaced over sequences and queries")
+    token_stride = q.stride(1) if q_len > 1 else q.stride(0)
+    _kv4_tensor(where, "out", out, "bfloat16", q.numel())
+    _kv4_tensor(where, "lengths", lengths, "int32", B)
+    if out.shape != q.shape:
+        raise ValueError(f"{where}: out has q's shape")
+    if lse is not None:
+        _kv4_tensor(where, "lse", lse, "float32", B * q_heads * q_len)
+    nbytes = 0
+    if workspace is not None:
+        _kv4_tensor(where, "workspace", workspace, "uint8", 0)
+        nbytes = workspace.numel()
+    flags = (ULYSSES_KV4_CAUSAL if causal else 0) | (ULYSSES_KV4_WEIGHTS if weights else 0)
+    _check(load().ulysses_kv4_attn(kv.handle, _ptr(cache), _ptr(q), q_heads, q_len, token_stride, q.stride(2),
+                                   _ptr(out), _ptr(lse), _ptr(lengths), float(softmax_scale), flags, _ptr(workspace),
+                                   nbytes, _stream(stream)), where)
+
+
+def ulysses_kv4_evict(src_kv: KV4Plan, src_cache, dst_kv: KV4Plan, dst_cache, lengths, new_lengths, keep: int,
+                      sink: int = 0, recent: int = 0, stream=None) -> None:
+    """Move the slots worth keeping (the first `sink`, the last `recent` and
+    those of largest accumulated weight, `keep` in all) into dst_cache, in
+    their order; new_lengths [batch] gets min(lengths, keep)."""
+    where = "ulysses_kv4_evict"
+    _kv4_tensor(where, "src_cache", src_cache, "uint8", src_kv.cache_bytes)
+    _kv4_tensor(where, "dst_cache", dst_cache, "uint8", dst_kv.cache_bytes)
+    _kv4_tensor(where, "lengths", lengths, "int32", src_kv.batch)
+    _kv4_tensor(where, "new_lengths", new_lengths, "int32", src_kv.batch)
+    _check(load().ulysses_kv4_evict(src_kv.handle, _ptr(src_cache), dst_kv.handle, _ptr(dst_cache), _ptr(lengths),
+                                    _ptr(new_lengths), int(keep), int(sink), int(recent), _stream(stream)), where)
+
+
+def ulysses_kv4_last_device_error(kv: KV4Plan, stream=None) -> int:
+    return load().ulysses_kv4_last_device_error(kv.handle, _stream(stream))

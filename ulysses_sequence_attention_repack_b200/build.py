@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libulysses.so")
 # so the product library exports only what include/ulysses.h declares
 SELFTEST_LIB = os.path.join(PKG, "libulysses_selftest.so")
 DEBUG_LIB = os.path.join(PKG, "libulysses_debug.so")
-SOURCES = ["api.cpp", "repack.cu", "prologue.cu", "attn_fwd.cu", "attn_bwd.cu", "noalloc.cu", "transport.cu"]
+SOURCES = ["api.cpp", "repack.cu", "prologue.cu", "attn_fwd.cu", "attn_bwd.cu", "noalloc.cu", "transport.cu",
+           "kv4_api.cpp", "kv4_cache.cu", "kv4_attn.cu"]
 SELFTEST_SOURCES = ["selftest.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

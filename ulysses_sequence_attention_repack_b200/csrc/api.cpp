@@ -2,7 +2,6 @@
 // launch sequence of the three steps.  Declarations and argument contracts
 // are in include/ulysses.h.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <cmath>
@@ -11,48 +10,21 @@
 #include <mutex>
 #include <new>
 
+#include "api_util.h"
 #include "internal.h"
 
+using ulysses::align_up;
+using ulysses::aligned16;
+using ulysses::NvtxRange;
+using ulysses::overlap;
+using ulysses::status_of;
+
 namespace {
-
-// NVTX ranges (domain "ulysses") around every launching entry point and
-// around the three steps inside the layer calls, so a timeline profiler
-// shows repack -> attention -> inverse repack.  Without a profiler attached
-// a range costs one function-pointer check.
-nvtxDomainHandle_t nvtx_domain() {
-  static const nvtxDomainHandle_t d = nvtxDomainCreateA("ulysses");
-  return d;
-}
-
-class NvtxRange {
- public:
-  explicit NvtxRange(const char* name) {
-    nvtxEventAttributes_t a;
-    std::memset(&a, 0, sizeof(a));
-    a.version = NVTX_VERSION;
-    a.size = NVTX_EVENT_ATTRIB_STRUCT_SIZE;
-    a.messageType = NVTX_MESSAGE_TYPE_ASCII;
-    a.message.ascii = name;
-    nvtxDomainRangePushEx(nvtx_domain(), &a);
-  }
-  ~NvtxRange() { nvtxDomainRangePop(nvtx_domain()); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
 
 constexpr int32_t kHeadDim = 128;
 constexpr int32_t kMaxHeads = 1024;
 constexpr int32_t kMaxPlanes = 8;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 4096;   // kernels index rows with int32
-
-inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-inline bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + static_cast<uintptr_t>(bbytes) && y < x + static_cast<uintptr_t>(abytes);
-}
 
 // bytes spanned by the sequence-sharded buffer with the given strides
 inline int64_t seq_extent_bytes(const ulysses_plan_t* p, int32_t planes, int64_t tok, int64_t pl) {
@@ -73,12 +45,6 @@ int device_ready(const ulysses_plan_t* p) {
     return ULYSSES_ERR_CUDA;
   }
   return dev == p->device ? ULYSSES_OK : ULYSSES_ERR_ARG;
-}
-
-int status_of(cudaError_t e) {
-  if (e == cudaSuccess) return ULYSSES_OK;
-  cudaGetLastError();
-  return ULYSSES_ERR_CUDA;
 }
 
 int repack_fwd_impl(const ulysses_plan_t* p, const void* src, void* dst, cudaStream_t st) {

@@ -56,6 +56,14 @@ struct ulysses_plan_s {
   ulysses::HostPipe* pipe;              // created by the first ulysses_layer_fwd_host call
 };
 
+// The geometry of 4-bit K/V caches (kv4.cuh), and a device error word.
+struct ulysses_kv4_s {
+  int32_t B, H;             // sequences, K/V heads
+  int64_t cap;              // slots of a (sequence, head) pair, a multiple of 32
+  int32_t device;           // device of the error word (-1: none)
+  unsigned int* dev_err;
+};
+
 namespace ulysses {
 
 // One repack launch over planes [c0, c0 + cc).
@@ -136,5 +144,70 @@ struct AttnBwdLaunch {
 };
 
 cudaError_t launch_attn_bwd(const AttnBwdLaunch& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- 4-bit K/V cache
+
+// bf16 K and V rows of a packed batch: element d of row i and head h is at
+// i * token_stride + (h / heads_per_rank) * rank_stride + (h % heads_per_rank) * head_stride + d;
+// rows [cu[b], cu[b + 1]) are sequence b's, in slots start[b] on.
+struct Kv4Rows {
+  void* k;
+  void* v;
+  int64_t rows;
+  int64_t token_stride, head_stride, rank_stride;
+  int32_t heads_per_rank;
+  const int32_t* cu;
+  const int32_t* start;
+  const int32_t* pos0;      // append: position of each sequence's first new row; null: its slot
+};
+
+struct Kv4RowsLaunch {
+  Kv4Rows r;
+  int32_t B, H;
+  int64_t cap;
+  uint8_t* cache;
+  float* weight;
+  int32_t* pos;
+  int64_t blocks_bytes;     // extent of the blocks, for the bounds-checked build
+  unsigned int* err;
+};
+
+cudaError_t launch_kv4_rows(bool load, const Kv4RowsLaunch& a, cudaStream_t stream);
+
+struct Kv4EvictLaunch {
+  int32_t B, H;
+  int64_t src_cap, dst_cap;
+  const uint8_t* src;
+  const float* src_weight;
+  const int32_t* src_pos;
+  uint8_t* dst;
+  float* dst_weight;
+  int32_t* dst_pos;
+  const int32_t* lengths;
+  int32_t* new_lengths;
+  int32_t keep, sink, recent;
+  unsigned int* err;
+};
+
+cudaError_t launch_kv4_evict(const Kv4EvictLaunch& a, cudaStream_t stream);
+
+struct Kv4AttnLaunch {
+  int32_t B, H, G, Lq;      // sequences, K/V heads, query heads of each, queries of a sequence
+  int64_t cap;
+  const uint8_t* cache;
+  float* weight;            // accumulated weights of the cache; null: they are not kept
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  void* out;                // [B * Lq, H * G, 128] bf16
+  float* lse;               // [B, H * G, Lq], or null
+  const int32_t* lengths;
+  float scale;
+  int32_t causal;
+  uint8_t* workspace;
+  unsigned int* err;
+};
+
+int64_t kv4_attn_workspace_bytes(int32_t B, int32_t H, int32_t G, int32_t Lq, int64_t cap, bool weights);
+cudaError_t launch_kv4_attn(const Kv4AttnLaunch& a, cudaStream_t stream);
 
 }  // namespace ulysses

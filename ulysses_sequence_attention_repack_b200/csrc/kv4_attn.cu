@@ -1,0 +1,658 @@
+// Attention of new tokens over a 4-bit K/V cache (kv4.cuh).
+//
+// Row r of a K/V head is query token r / G of the sequence and its query head
+// h * G + r % G.  With a slot's K row held as m_w + s_w n (group w = d / 64),
+//
+//   z_rt = scale q_r . k_t = scale sum_w ( s_tw (q_rw . n_tw) + m_tw sum_d q_rwd )
+//   o_r  = sum_t p_rt v_t  = sum_t (p_rt s_tw) n_t + sum_t p_rt m_tw,   p = softmax z
+//
+// so the products run on the codes, and scales and minima are applied to
+// their fp32 results.  The work is bound by the cache's bytes (144 a slot), so
+// what counts is that a slot's 256 codes cost few instructions:
+//
+// - A code becomes an fp16 number by one AND: fp16 bits 0 .. 15 are the
+//   subnormal n 2^-24, and bits n << 4 are 16 n 2^-24 (both exact, and the
+//   tensor core multiplies subnormals exactly).  The factors 16 are taken out
+//   of the query (K) and of the finished sums (V), and 2^-24 with the scale.
+// - z^T = K q^T is a 16 x 8 x 16 product with slots as rows: 8 query rows a
+//   product, so that up to 8 rows (one query head, or a group of them) cost
+//   the same.  The lanes that hold z^T hold the same two query rows as those
+//   of o^T = V^T p^T, so the running maximum and sums need no exchange, and p
+//   becomes an operand of the second product by one 8 x 8 transpose.
+// - The maximum in the exponent is replaced only when a row's grows by more
+//   than 2^8, and the power of two that keeps p s inside fp16 only when the
+//   scales grow 4-fold, so most steps neither exchange nor rescale anything.
+//
+// Roundings: q, codes, scales and minima enter exactly (q by a power of two,
+// which keeps its 8 bits down to 2^-28 of the row's largest); z, p, maxima and
+// sums are fp32; p s is rounded to fp16 for the second product (2^-11, for
+// twice the precision that bf16 would keep); o is rounded once, to bf16.
+//
+// Work split: the tiles of 128 slots of all (sequence, K/V head, block of
+// query rows) are one list, cut into equal runs, one a CTA, so ragged lengths
+// and few heads fill the GPU alike.  Each of a CTA's four warps takes one
+// 32-slot block of a tile.  Where a run ends inside a pair the CTA leaves an
+// unfinished sum with its maximum in the workspace, and a second kernel joins
+// them.  The lists are found from the lengths on the device, so that a
+// captured launch stays right when they change.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "bounds.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+
+namespace ulysses {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kTile = kWarps * kKv4BlockSlots;   // slots of a tile
+constexpr int kMaxBatch = 1024;
+constexpr int kSmsMax = 148;
+constexpr int kCtasPerSm = 4;
+constexpr int kMaxCtas = kSmsMax * kCtasPerSm;   // sizes the workspace; the grid never passes it
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.f;                     // log2 by which a maximum may be passed before it moves
+constexpr int kHeadroom = 5;                     // p s 2^(5 - c) <= 2^8 2^2 2^5: inside fp16
+
+struct Args {
+  const uint8_t* cache;
+  float* weight;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const int32_t* lengths;
+  float* part_o;      // [2 * CTAs][rows of a block][128]: unfinished sums
+  float2* part_ml;    // [2 * CTAs][rows of a block]: their maxima and sums of p
+  float* row_lse;     // [B * H][R]: log2 of the sums, for the weights
+  float* logits;      // [B * H][R][cap]: z log2 e of the slots, for the weights
+  int64_t cap, q_token_stride, q_head_stride;
+  int32_t B, H, G, Lq, R, RB;
+  float scale_log2;
+  int32_t causal;
+  unsigned int* err;
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+#define NEG_INF __int_as_float(0xff800000)
+
+// ---------------------------------------------------------------- the list of tiles
+
+// prefix[b] = tiles of the sequences before b, over all heads and row blocks.
+// Every thread of the block calls it.
+__device__ __forceinline__ void tile_prefix(const Args& a, int32_t* prefix, bool report) {
+  __shared__ int32_t sums[kThreads / 32];
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = threadIdx.x * per + i;
+    if (b < a.B) mine += (kv4_length(a.lengths[b], a.cap, report ? a.err : nullptr) + kTile - 1) / kTile;
+  }
+  int x = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) sums[w] = x;
+  __syncthreads();
+  int before = x - mine;
+  for (int i = 0; i < w; ++i) before += sums[i];
+  const int per_tile = a.H * a.RB;
+  for (int i = 0; i < per; ++i) {
+    const int b = threadIdx.x * per + i;
+    if (b >= a.B) break;
+    prefix[b] = before * per_tile;
+    before += (kv4_length(a.lengths[b], a.cap, nullptr) + kTile - 1) / kTile;
+    if (b == a.B - 1) prefix[a.B] = before * per_tile;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int tiles_per_cta(int total, int ctas) { return (total + ctas - 1) / ctas; }
+
+// ---------------------------------------------------------------- main kernel
+
+template <int NT, bool kWeights>
+__global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Args a) {
+  constexpr int RPB = 8 * NT;
+  __shared__ int32_t prefix[kMaxBatch + 1];
+  __shared__ __align__(16) float mo[kWarps][RPB][kKv4Dim];
+  __shared__ float mM[kWarps][RPB], ml[kWarps][RPB];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+
+  tile_prefix(a, prefix, blockIdx.x == 0);
+  const int total = prefix[a.B];
+  const int chunk = tiles_per_cta(total, gridDim.x);
+  const int64_t first64 = static_cast<int64_t>(blockIdx.x) * chunk;
+  if (first64 >= total) return;
+  int tile = static_cast<int>(first64);
+  const int tile_end = min(total, tile + chunk);
+  const int run_begin = tile;
+
+  while (tile < tile_end) {
+    // the fragment: tiles [lo, hi) of one (sequence, head, row block)
+    int b;
+    {
+      int l = 0, h = a.B;
+      while (h - l > 1) {
+        const int mid = (l + h) >> 1;
+        if (prefix[mid] <= tile)
+          l = mid;
+        else
+          h = mid;
+      }
+      b = l;
+    }
+    const int len = kv4_length(a.lengths[b], a.cap, nullptr);
+    const int ntiles = (len + kTile - 1) / kTile;
+    const int unit = (tile - prefix[b]) / ntiles;
+    const int lo = (tile - prefix[b]) - unit * ntiles;
+    const int hi = min(ntiles, lo + tile_end - tile);
+    const int h = unit / a.RB, rb = unit - h * a.RB;
+    const int64_t bh = static_cast<int64_t>(b) * a.H + h;
+    const int row0 = rb * RPB;
+    const uint8_t* pair = a.cache + bh * (a.cap / kKv4BlockSlots) * kKv4BlockBytes;
+
+    // the query as the second operand of z^T = K q^T: this lane holds, of row
+    // row0 + 8 nt + g, dims 16t .. 16t + 15 of each group, scaled by a power of
+    // two that takes the row's largest into [2^14, 2^15)
+    uint32_t qf[NT][16];
+    float qscale[NT][2], qsum[NT][2][2];
+    int limit[NT][2];
+    int lowest = len;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + 8 * nt + g;
+      float f[2][16];
+      if (r < a.R) {
+        const int i = r / a.G;
+        const uint16_t* src = a.q + (static_cast<int64_t>(b) * a.Lq + i) * a.q_token_stride +
+                              static_cast<int64_t>(h * a.G + (r - i * a.G)) * a.q_head_stride;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + 64 * w + 16 * t + 8 * v);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[w][8 * v + 2 * e] = bf16_lo(u[e]);
+              f[w][8 * v + 2 * e + 1] = bf16_hi(u[e]);
+            }
+          }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[0][e] = f[1][e] = 0.f;
+      }
+      uint32_t top = 0;   // bits of the largest magnitude: NaN and infinity rank above every number
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(f[w][e]) & 0x7fffffffu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int k = static_cast<int>(top >> 23) - 127;
+      const int e = max(-100, min(100, 14 - k));
+      const float up = pow2(e);
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          f[w][i] *= up;
+          sum[w] += f[w][i];
+        }
+      // word v of the lane's 16-byte K load: group v & 1, dims 16t + 8 (v >> 1) + 0 .. 7
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float* x = &f[v & 1][8 * (v >> 1)];
+        qf[nt][4 * v] = pack_f16(x[0], x[4]);
+        qf[nt][4 * v + 1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
+        qf[nt][4 * v + 2] = pack_f16(x[2], x[6]);
+        qf[nt][4 * v + 3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 1);
+        sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 2);
+        sum[w] *= 0x1p-24f;
+      }
+      // a row with an infinity or a NaN has no softmax: its logits are NaN
+      const float qs = top >= 0x7f800000u ? __int_as_float(0x7fc00000) : a.scale_log2 * pow2(24 - e);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {   // to the lanes that hold this row's z: rows 2t and 2t + 1
+        const int from = 4 * (2 * t + c);
+        qscale[nt][c] = __shfl_sync(0xffffffffu, qs, from);
+        qsum[nt][c][0] = __shfl_sync(0xffffffffu, sum[0], from);
+        qsum[nt][c][1] = __shfl_sync(0xffffffffu, sum[1], from);
+        const int rr = row0 + 8 * nt + 2 * t + c;
+        limit[nt][c] = rr < a.R ? (a.causal ? max(0, len - a.Lq + rr / a.G + 1) : len) : 0;
+        if (rr < a.R) lowest = min(lowest, limit[nt][c]);
+      }
+    }
+    lowest = __reduce_min_sync(0xffffffffu, lowest);
+
+    float acc[NT][8][4];
+    float M[NT][2], Ms[NT][2], l[NT][2], z0[NT][2][2];   // Ms: M, or 0 while M is -inf
+    int c_exp[2] = {-100, -100};
+    float s_limit[2] = {pow2(-98), pow2(-98)}, s_up[2] = {pow2(kHeadroom + 100), pow2(kHeadroom + 100)};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        M[nt][c] = NEG_INF;
+        Ms[nt][c] = l[nt][c] = z0[nt][c][0] = z0[nt][c][1] = 0.f;
+      }
+    }
+
+    for (int tl = lo; tl < hi; ++tl) {
+      const int slot0 = tl * kTile + warp * kKv4BlockSlots;
+      if (slot0 >= len) break;
+      const uint8_t* blk = pair + static_cast<int64_t>(slot0 / kKv4BlockSlots) * kKv4BlockBytes;
+      const bool edge = slot0 + kKv4BlockSlots > lowest;
+      uint4 meta[2][2];
+      float s[NT][2][4];   // z log2 e: [16-slot half][slot g row 2t, g 2t+1, g+8 2t, g+8 2t+1]
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint4 ka = *reinterpret_cast<const uint4*>(blk + (16 * mt + g) * 64 + t * 16);
+        const uint4 kb = *reinterpret_cast<const uint4*>(blk + (16 * mt + g + 8) * 64 + t * 16);
+        meta[mt][0] = *reinterpret_cast<const uint4*>(blk + kKv4MetaOffset + (16 * mt + g) * 16);
+        meta[mt][1] = *reinterpret_cast<const uint4*>(blk + kKv4MetaOffset + (16 * mt + g + 8) * 16);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        float d[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) d[nt][0][c] = d[nt][1][c] = 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t xa = wa[v] >> 8, xb = wb[v] >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(d[nt][v & 1], wa[v] & kLow, wb[v] & kLow, wa[v] & kHigh, wb[v] & kHigh, qf[nt][4 * v],
+                qf[nt][4 * v + 1]);
+            mma(d[nt][v & 1], xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[nt][4 * v + 2], qf[nt][4 * v + 3]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4& m = meta[mt][c >> 1];
+            const int row = c & 1;
+            float x = bf16_lo(m.x) * d[nt][0][c];
+            x = fmaf(bf16_hi(m.x), qsum[nt][row][0], x);
+            x = fmaf(bf16_lo(m.y), d[nt][1][c], x);
+            x = fmaf(bf16_hi(m.y), qsum[nt][row][1], x);
+            x *= qscale[nt][row];
+            const int slot = slot0 + 16 * mt + g + 8 * (c >> 1);
+            if (edge && slot >= limit[nt][row]) x = NEG_INF;
+            s[nt][mt][c] = x;
+            if (kWeights) {
+              const int r = row0 + 8 * nt + 2 * t + row;
+              if (r < a.R && slot < len) a.logits[(bh * a.R + r) * a.cap + slot] = x;
+            }
+          }
+      }
+      // slots behind the length hold anything: nothing of them may reach a sum
+      if (edge) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (slot0 + 16 * mt + g + 8 * i >= len) meta[mt][i] = make_uint4(0, 0, 0, 0);
+      }
+      float vs[2][2][2];   // V scales [half][slot g, g + 8][group]
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          vs[mt][i][0] = bf16_lo(meta[mt][i].z);
+          vs[mt][i][1] = bf16_lo(meta[mt][i].w);
+        }
+      float top[NT][2];
+      bool move = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[nt][c] = fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2]));
+          move |= top[nt][c] > M[nt][c] + kGrow;
+        }
+      float big[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        big[w] = fmaxf(fmaxf(vs[0][0][w], vs[0][1][w]), fmaxf(vs[1][0][w], vs[1][1][w]));
+        move |= big[w] > s_limit[w];
+      }
+      if (__any_sync(0xffffffffu, move)) {
+        float down[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          // scales are not negative, so their bits order them
+          const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(big[w]));
+          const int c_new = max(c_exp[w], max(-100, min(100, static_cast<int>(m >> 23) - 127)));
+          down[w] = ex2(static_cast<float>(c_exp[w] - c_new));
+          c_exp[w] = c_new;
+          s_limit[w] = pow2(c_new + 2);
+          s_up[w] = pow2(kHeadroom - c_new);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float m = top[nt][c];
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            const float m_new = fmaxf(M[nt][c], m);
+            const float al = m_new == M[nt][c] ? 1.f : ex2(M[nt][c] - m_new);
+            M[nt][c] = m_new;
+            Ms[nt][c] = m_new == NEG_INF ? 0.f : m_new;
+            l[nt][c] *= al;
+            z0[nt][c][0] *= al;
+            z0[nt][c][1] *= al;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[nt][i][c] *= al * down[i >> 2];
+              acc[nt][i][c + 2] *= al * down[i >> 2];
+            }
+          }
+      }
+      // p, its sums, and p s as the operand of the second product
+      uint32_t pb[2][NT][2][2];   // [group][row block][half][operand register]
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          float w0[4], w1[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = c >> 1, row = c & 1;
+            const float p = ex2(s[nt][mt][c] - Ms[nt][row]);
+            l[nt][row] += p;
+            const uint4& m = meta[mt][i];
+            w0[c] = p * (vs[mt][i][0] * s_up[0]);
+            w1[c] = p * (vs[mt][i][1] * s_up[1]);
+            float m0 = bf16_hi(m.z), m1 = bf16_hi(m.w);
+            if (edge && slot0 + 16 * mt + g + 8 * i >= limit[nt][row]) w0[c] = w1[c] = m0 = m1 = 0.f;
+            z0[nt][row][0] = fmaf(p, m0, z0[nt][row][0]);
+            z0[nt][row][1] = fmaf(p, m1, z0[nt][row][1]);
+          }
+          pb[0][nt][mt][0] = transpose8x8(pack_f16(w0[0], w0[1]));
+          pb[0][nt][mt][1] = transpose8x8(pack_f16(w0[2], w0[3]));
+          pb[1][nt][mt][0] = transpose8x8(pack_f16(w1[0], w1[1]));
+          pb[1][nt][mt][1] = transpose8x8(pack_f16(w1[2], w1[3]));
+        }
+      // o^T += V^T p^T: this lane holds dims 8g .. 8g + 7 of each group, and
+      // slots 2t, 2t + 1 and 2t + 8, 2t + 9 of the half are the pairs of its registers
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint8_t* vrow = blk + kKv4VOffset + (16 * mt + 2 * t) * 64 + g * 8;
+        const uint2 v0 = *reinterpret_cast<const uint2*>(vrow), v1 = *reinterpret_cast<const uint2*>(vrow + 64);
+        const uint2 v8 = *reinterpret_cast<const uint2*>(vrow + 512), v9 = *reinterpret_cast<const uint2*>(vrow + 576);
+        const uint32_t A[2] = {v0.x, v0.y}, B[2] = {v1.x, v1.y}, C[2] = {v8.x, v8.y}, D[2] = {v9.x, v9.y};
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t sel = half ? 0x7632u : 0x5410u;
+            uint32_t x = __byte_perm(A[w], B[w], sel), y = __byte_perm(C[w], D[w], sel);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int i = 4 * w + 2 * half + j;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma(acc[nt][i], x & kLow, x & kHigh, y & kLow, y & kHigh, pb[w][nt][mt][0], pb[w][nt][mt][1]);
+              x >>= 8;
+              y >>= 8;
+            }
+          }
+      }
+    }
+
+    // the fragment's sums: over the lanes that hold the same rows, then over the warps
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int dlt = 4; dlt < 32; dlt <<= 1) {
+          l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], dlt);
+          z0[nt][c][0] += __shfl_xor_sync(0xffffffffu, z0[nt][c][0], dlt);
+          z0[nt][c][1] += __shfl_xor_sync(0xffffffffu, z0[nt][c][1], dlt);
+        }
+        const int row = 8 * nt + 2 * t + c;
+        if (g == 0) {
+          mM[warp][row] = M[nt][c];
+          ml[warp][row] = l[nt][c];
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          // codes 2^-24, p s 2^(5 - c); the odd nibbles carry a further 16
+          const float even = pow2(24 - kHeadroom) * pow2(c_exp[w]), odd = even * 0.0625f, zz = z0[nt][c][w];
+          float4* dst = reinterpret_cast<float4*>(&mo[warp][row][64 * w + 8 * g]);
+          dst[0] = make_float4(fmaf(acc[nt][4 * w][c], even, zz), fmaf(acc[nt][4 * w][c + 2], odd, zz),
+                               fmaf(acc[nt][4 * w + 1][c], even, zz), fmaf(acc[nt][4 * w + 1][c + 2], odd, zz));
+          dst[1] = make_float4(fmaf(acc[nt][4 * w + 2][c], even, zz), fmaf(acc[nt][4 * w + 2][c + 2], odd, zz),
+                               fmaf(acc[nt][4 * w + 3][c], even, zz), fmaf(acc[nt][4 * w + 3][c + 2], odd, zz));
+        }
+      }
+    __syncthreads();
+    const bool whole = lo == 0 && hi == ntiles;
+    const int part = 2 * blockIdx.x + (tile == run_begin ? 0 : 1);
+    const int d = threadIdx.x;
+    for (int row = 0; row < RPB && row0 + row < a.R; ++row) {
+      float Mt = NEG_INF;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) Mt = fmaxf(Mt, mM[w][row]);
+      const float base = Mt == NEG_INF ? 0.f : Mt;
+      float o = 0.f, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(mM[w][row] - base);
+        o = fmaf(f, mo[w][row][d], o);
+        sum = fmaf(f, ml[w][row], sum);
+      }
+      const int r = row0 + row;
+      if (whole) {
+        const int i = r / a.G, hq = h * a.G + (r - i * a.G);
+        const float y = sum == 0.f ? 0.f : o / sum;
+        a.out[((static_cast<int64_t>(b) * a.Lq + i) * a.H * a.G + hq) * kKv4Dim + d] =
+            __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        if (d == 0) {
+          const float ls = sum == 0.f ? NEG_INF : Mt + log2f(sum);
+          if (a.lse) a.lse[(static_cast<int64_t>(b) * a.H * a.G + hq) * a.Lq + i] = ls;
+          if (kWeights) a.row_lse[bh * a.R + r] = ls;
+        }
+      } else {
+        a.part_o[(static_cast<int64_t>(part) * RPB + row) * kKv4Dim + d] = o;
+        if (d == 0) a.part_ml[part * RPB + row] = make_float2(Mt, sum);
+      }
+    }
+    __syncthreads();
+    tile += hi - lo;
+  }
+}
+
+// ---------------------------------------------------------------- joining the parts
+
+// One block per row.  A row whose tiles one CTA held is done already.
+template <int RPB>
+__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Args a, int ctas) {
+  __shared__ int32_t prefix[kMaxBatch + 1];
+  tile_prefix(a, prefix, false);
+  const int64_t x = blockIdx.x;
+  const int64_t bh = x / a.R;
+  const int r = static_cast<int>(x - bh * a.R);
+  const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+  const int rb = r / RPB, row = r - rb * RPB;
+  const int d = threadIdx.x;
+  const int i = r / a.G, hq = h * a.G + (r - i * a.G);
+  const int64_t at = ((static_cast<int64_t>(b) * a.Lq + i) * a.H * a.G + hq) * kKv4Dim + d;
+  const int64_t lse_at = (static_cast<int64_t>(b) * a.H * a.G + hq) * a.Lq + i;
+  const int len = kv4_length(a.lengths[b], a.cap, nullptr);
+  const int ntiles = (len + kTile - 1) / kTile;
+  float o = 0.f, sum = 0.f, Mt = NEG_INF;
+  if (ntiles > 0) {
+    const int chunk = tiles_per_cta(prefix[a.B], ctas);
+    const int t0 = prefix[b] + (h * a.RB + rb) * ntiles, t1 = t0 + ntiles;
+    const int c0 = t0 / chunk, c1 = (t1 - 1) / chunk;
+    if (c0 == c1) return;
+    for (int c = c0; c <= c1; ++c) {
+      const int part = 2 * c + (c * chunk >= t0 ? 0 : 1);
+      Mt = fmaxf(Mt, a.part_ml[part * RPB + row].x);
+    }
+    const float base = Mt == NEG_INF ? 0.f : Mt;
+    for (int c = c0; c <= c1; ++c) {
+      const int part = 2 * c + (c * chunk >= t0 ? 0 : 1);
+      const float2 m = a.part_ml[part * RPB + row];
+      const float f = ex2(m.x - base);
+      o = fmaf(f, a.part_o[(static_cast<int64_t>(part) * RPB + row) * kKv4Dim + d], o);
+      sum = fmaf(f, m.y, sum);
+    }
+  }
+  a.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o / sum));
+  if (d == 0) {
+    const float ls = sum == 0.f ? NEG_INF : Mt + log2f(sum);
+    if (a.lse) a.lse[lse_at] = ls;
+    if (a.row_lse) a.row_lse[bh * a.R + r] = ls;
+  }
+}
+
+// weight_t += sum_r 2^(z_rt - lse_r), the rows in their order.
+__global__ void __launch_bounds__(kThreads) kv4_weight_kernel(const Args a) {
+  const int64_t bh = blockIdx.y;
+  const int len = kv4_length(a.lengths[bh / a.H], a.cap, nullptr);
+  const float* lse = a.row_lse + bh * a.R;
+  for (int64_t slot = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; slot < len;
+       slot += static_cast<int64_t>(gridDim.x) * kThreads) {
+    float sum = 0.f;
+    for (int r = 0; r < a.R; ++r) {
+      const float x = lse[r];
+      if (x != NEG_INF) sum += ex2(a.logits[(bh * a.R + r) * a.cap + slot] - x);
+    }
+    a.weight[bh * a.cap + slot] += sum;
+  }
+}
+
+int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+
+int rows_of_block(int64_t R) { return R <= 8 ? 8 : 16; }
+
+template <int NT, bool kWeights>
+cudaError_t launch_main(const Args& a, int* ctas, cudaStream_t stream) {
+  int dev = 0, sms = 1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  *ctas = std::min(sms, kSmsMax) * (NT == 1 ? 4 : 3);
+  kv4_attn_kernel<NT, kWeights><<<*ctas, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Parts and their (maximum, sum) pairs; with weights also each row's log-sum
+// and the logits of every slot.
+int64_t kv4_attn_workspace_bytes(int32_t B, int32_t H, int32_t G, int32_t Lq, int64_t cap, bool weights) {
+  const int64_t R = static_cast<int64_t>(G) * Lq, rpb = rows_of_block(R);
+  int64_t n = up256(2 * kMaxCtas * rpb * kKv4Dim * 4) + up256(2 * kMaxCtas * rpb * 8);
+  if (weights) n += up256(static_cast<int64_t>(B) * H * R * 4) + static_cast<int64_t>(B) * H * R * cap * 4;
+  return n;
+}
+
+cudaError_t launch_kv4_attn(const Kv4AttnLaunch& p, cudaStream_t stream) {
+  const int64_t R = static_cast<int64_t>(p.G) * p.Lq;
+  const int rpb = rows_of_block(R);
+  Args a;
+  a.cache = p.cache;
+  a.weight = p.weight;
+  a.q = static_cast<const uint16_t*>(p.q);
+  a.out = static_cast<uint16_t*>(p.out);
+  a.lse = p.lse;
+  a.lengths = p.lengths;
+  uint8_t* w = p.workspace;
+  a.part_o = reinterpret_cast<float*>(w);
+  w += up256(static_cast<int64_t>(2) * kMaxCtas * rpb * kKv4Dim * 4);
+  a.part_ml = reinterpret_cast<float2*>(w);
+  w += up256(static_cast<int64_t>(2) * kMaxCtas * rpb * 8);
+  a.row_lse = p.weight ? reinterpret_cast<float*>(w) : nullptr;
+  w += up256(static_cast<int64_t>(p.B) * p.H * R * 4);
+  a.logits = p.weight ? reinterpret_cast<float*>(w) : nullptr;
+  a.cap = p.cap;
+  a.q_token_stride = p.q_token_stride;
+  a.q_head_stride = p.q_head_stride;
+  a.B = p.B;
+  a.H = p.H;
+  a.G = p.G;
+  a.Lq = p.Lq;
+  a.R = static_cast<int32_t>(R);
+  a.RB = static_cast<int32_t>((R + rpb - 1) / rpb);
+  a.scale_log2 = p.scale * kLog2e;
+  a.causal = p.causal;
+  a.err = p.err;
+  int ctas = 0;
+  cudaError_t e;
+  if (rpb == 8)
+    e = p.weight ? launch_main<1, true>(a, &ctas, stream) : launch_main<1, false>(a, &ctas, stream);
+  else
+    e = p.weight ? launch_main<2, true>(a, &ctas, stream) : launch_main<2, false>(a, &ctas, stream);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(p.B) * p.H * R;
+  if (rpb == 8)
+    kv4_join_kernel<8><<<static_cast<unsigned>(rows), kThreads, 0, stream>>>(a, ctas);
+  else
+    kv4_join_kernel<16><<<static_cast<unsigned>(rows), kThreads, 0, stream>>>(a, ctas);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !p.weight) return e;
+  const int64_t pairs = static_cast<int64_t>(p.B) * p.H;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((p.cap + kThreads - 1) / kThreads,
+                                                              (8 * kSmsMax + pairs - 1) / pairs * 2));
+  kv4_weight_kernel<<<dim3(static_cast<unsigned>(want), static_cast<unsigned>(pairs)), kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace ulysses
