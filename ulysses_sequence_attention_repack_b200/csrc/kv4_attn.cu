@@ -46,6 +46,7 @@
 #include "bounds.cuh"
 #include "internal.h"
 #include "kv4.cuh"
+#include "sm100_ptx.cuh"
 
 namespace ulysses {
 namespace {
@@ -54,6 +55,8 @@ constexpr int kThreads = 128;
 constexpr int kWarps = 4;
 constexpr int kTile = kWarps * kKv4BlockSlots;   // slots of a tile
 constexpr int kMaxBatch = 1024;
+constexpr int kStages = 2;                       // blocks a warp has in flight
+constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
 constexpr int kSmsMax = 148;
 constexpr int kCtasPerSm = 4;
 constexpr int kMaxCtas = kSmsMax * kCtasPerSm;   // sizes the workspace; the grid never passes it
@@ -147,18 +150,94 @@ __device__ __forceinline__ void tile_prefix(const Args& a, int32_t* prefix, bool
 
 __device__ __forceinline__ int tiles_per_cta(int total, int ctas) { return (total + ctas - 1) / ctas; }
 
+// A place in the list: tile `lo` of `ntiles` of one (sequence, head, row block).
+struct Place {
+  int b, len, ntiles, unit, lo;
+
+  __device__ __forceinline__ void find(const Args& a, const int32_t* prefix, int tile) {
+    int l = 0, h = a.B;   // prefix[l] <= tile < prefix[h], so the sequence found has tiles
+    while (h - l > 1) {
+      const int mid = (l + h) >> 1;
+      if (prefix[mid] <= tile)
+        l = mid;
+      else
+        h = mid;
+    }
+    b = l;
+    len = kv4_length(a.lengths[b], a.cap, nullptr);
+    ntiles = (len + kTile - 1) / kTile;
+    unit = (tile - prefix[b]) / ntiles;
+    lo = (tile - prefix[b]) - unit * ntiles;
+  }
+};
+
+// The blocks that one warp takes of a CTA's run, copied ahead into its ring.
+struct Feed {
+  Place at;
+  int tile, end;
+  const uint8_t* pair;
+  uint32_t issued, ring, bars;
+
+  __device__ __forceinline__ void locate(const Args& a) {
+    pair = a.cache + (static_cast<int64_t>(at.b) * a.H + at.unit / a.RB) * (a.cap / kKv4BlockSlots) * kKv4BlockBytes;
+  }
+  // Starts the copy of the next block, if there is one.  A whole block is
+  // copied even where the length ends inside it: it lies in the cache.
+  __device__ __forceinline__ void next(const Args& a, const int32_t* prefix, int warp, int lane) {
+    while (tile < end) {
+      const int block = at.lo * kWarps + warp;
+      const bool exists = block * kKv4BlockSlots < at.len;
+      if (exists) {
+        if (lane == 0) {
+          const uint32_t s = issued % kStages, bar = bars + 8 * s;
+          mbar_arrive_expect_tx(bar, kKv4BlockBytes);
+          bulk_load(ring + s * kKv4BlockBytes, pair + static_cast<int64_t>(block) * kKv4BlockBytes, kKv4BlockBytes,
+                    bar);
+        }
+        ++issued;
+      }
+      ++tile;
+      if (++at.lo == at.ntiles && tile < end) {
+        at.find(a, prefix, tile);
+        locate(a);
+      }
+      if (exists) return;
+    }
+  }
+};
+
 // ---------------------------------------------------------------- main kernel
 
+// Dynamic shared memory: the warps' rings, then their sums [warp][row][128],
+// maxima and sums of p [warp][row], then the prefix of tiles.
+__host__ __device__ inline int smem_rows(int R, int RPB) { return R < RPB ? R : RPB; }
+__host__ __device__ inline int64_t smem_bytes(int R, int RPB, int B) {
+  return kWarps * (kStages * kKv4BlockBytes + smem_rows(R, RPB) * (kKv4Dim * 4 + 8)) + (B + 1) * 4;
+}
+
 template <int NT, bool kWeights>
-__global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(const Args a) {
   constexpr int RPB = 8 * NT;
-  __shared__ int32_t prefix[kMaxBatch + 1];
-  __shared__ __align__(16) float mo[kWarps][RPB][kKv4Dim];
-  __shared__ float mM[kWarps][RPB], ml[kWarps][RPB];
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bar_mem[kWarps][kStages];
+  __shared__ int abort_mem, drain_mem;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
+  const int mrows = smem_rows(a.R, RPB);
+  uint8_t* ring = smem + warp * kStages * kKv4BlockBytes;
+  float* mo = reinterpret_cast<float*>(smem + kWarps * kStages * kKv4BlockBytes);   // [warp][mrows][128]
+  float* mM = mo + kWarps * mrows * kKv4Dim;
+  float* ml = mM + kWarps * mrows;
+  int32_t* prefix = reinterpret_cast<int32_t*>(ml + kWarps * mrows);
 
-  tile_prefix(a, prefix, blockIdx.x == 0);
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    abort_mem = drain_mem = 0;
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bar_mem[0][0]) + 8 * i, 1);
+    fence_mbar_init();
+  }
+  tile_prefix(a, prefix, blockIdx.x == 0);   // (its barriers also order the initialisation above)
+  const WaitGuard guard{&abort_mem, a.err, kWaitLimitNs};
   const int total = prefix[a.B];
   const int chunk = tiles_per_cta(total, gridDim.x);
   const int64_t first64 = static_cast<int64_t>(blockIdx.x) * chunk;
@@ -167,29 +246,29 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Args a) {
   const int tile_end = min(total, tile + chunk);
   const int run_begin = tile;
 
+  Feed feed;
+  feed.at.find(a, prefix, tile);
+  feed.tile = tile;
+  feed.end = tile_end;
+  feed.locate(a);
+  feed.issued = 0;
+  feed.ring = smem_u32(ring);
+  feed.bars = smem_u32(&bar_mem[warp][0]);
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) feed.next(a, prefix, warp, lane);
+  uint32_t used = 0;        // blocks this warp has taken from its ring
+  uint32_t left_at = 0;     // the block whose copy did not come
+  bool alive = true;        // false once a wait has given up: nothing more is issued or waited for
+
   while (tile < tile_end) {
     // the fragment: tiles [lo, hi) of one (sequence, head, row block)
-    int b;
-    {
-      int l = 0, h = a.B;
-      while (h - l > 1) {
-        const int mid = (l + h) >> 1;
-        if (prefix[mid] <= tile)
-          l = mid;
-        else
-          h = mid;
-      }
-      b = l;
-    }
-    const int len = kv4_length(a.lengths[b], a.cap, nullptr);
-    const int ntiles = (len + kTile - 1) / kTile;
-    const int unit = (tile - prefix[b]) / ntiles;
-    const int lo = (tile - prefix[b]) - unit * ntiles;
+    Place at;
+    at.find(a, prefix, tile);
+    const int b = at.b, len = at.len, ntiles = at.ntiles, lo = at.lo;
     const int hi = min(ntiles, lo + tile_end - tile);
-    const int h = unit / a.RB, rb = unit - h * a.RB;
+    const int h = at.unit / a.RB, rb = at.unit - h * a.RB;
     const int64_t bh = static_cast<int64_t>(b) * a.H + h;
     const int row0 = rb * RPB;
-    const uint8_t* pair = a.cache + bh * (a.cap / kKv4BlockSlots) * kKv4BlockBytes;
 
     // the query as the second operand of z^T = K q^T: this lane holds, of row
     // row0 + 8 nt + g, dims 16t .. 16t + 15 of each group, scaled by a power of
@@ -290,7 +369,13 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Args a) {
     for (int tl = lo; tl < hi; ++tl) {
       const int slot0 = tl * kTile + warp * kKv4BlockSlots;
       if (slot0 >= len) break;
-      const uint8_t* blk = pair + static_cast<int64_t>(slot0 / kKv4BlockSlots) * kKv4BlockBytes;
+      const uint32_t stage = used % kStages;
+      if (alive && !mbar_wait_warp(feed.bars + 8 * stage, (used / kStages) & 1u, guard)) {
+        alive = false;
+        left_at = used;
+      }
+      ++used;
+      const uint8_t* blk = ring + stage * kKv4BlockBytes;
       const bool edge = slot0 + kKv4BlockSlots > lowest;
       uint4 meta[2][2];
       float s[NT][2][4];   // z log2 e: [16-slot half][slot g row 2t, g 2t+1, g+8 2t, g+8 2t+1]
@@ -451,6 +536,8 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Args a) {
             }
           }
       }
+      __syncwarp();   // every lane has read the block before it is replaced
+      if (alive) feed.next(a, prefix, warp, lane);
     }
 
     // the fragment's sums: over the lanes that hold the same rows, then over the warps
@@ -465,15 +552,16 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Args a) {
           z0[nt][c][1] += __shfl_xor_sync(0xffffffffu, z0[nt][c][1], dlt);
         }
         const int row = 8 * nt + 2 * t + c;
+        if (row >= mrows) continue;
         if (g == 0) {
-          mM[warp][row] = M[nt][c];
-          ml[warp][row] = l[nt][c];
+          mM[warp * mrows + row] = M[nt][c];
+          ml[warp * mrows + row] = l[nt][c];
         }
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           // codes 2^-24, p s 2^(5 - c); the odd nibbles carry a further 16
           const float even = pow2(24 - kHeadroom) * pow2(c_exp[w]), odd = even * 0.0625f, zz = z0[nt][c][w];
-          float4* dst = reinterpret_cast<float4*>(&mo[warp][row][64 * w + 8 * g]);
+          float4* dst = reinterpret_cast<float4*>(mo + (warp * mrows + row) * kKv4Dim + 64 * w + 8 * g);
           dst[0] = make_float4(fmaf(acc[nt][4 * w][c], even, zz), fmaf(acc[nt][4 * w][c + 2], odd, zz),
                                fmaf(acc[nt][4 * w + 1][c], even, zz), fmaf(acc[nt][4 * w + 1][c + 2], odd, zz));
           dst[1] = make_float4(fmaf(acc[nt][4 * w + 2][c], even, zz), fmaf(acc[nt][4 * w + 2][c + 2], odd, zz),
@@ -487,14 +575,14 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Args a) {
     for (int row = 0; row < RPB && row0 + row < a.R; ++row) {
       float Mt = NEG_INF;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) Mt = fmaxf(Mt, mM[w][row]);
+      for (int w = 0; w < kWarps; ++w) Mt = fmaxf(Mt, mM[w * mrows + row]);
       const float base = Mt == NEG_INF ? 0.f : Mt;
       float o = 0.f, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(mM[w][row] - base);
-        o = fmaf(f, mo[w][row][d], o);
-        sum = fmaf(f, ml[w][row], sum);
+        const float f = ex2(mM[w * mrows + row] - base);
+        o = fmaf(f, mo[(w * mrows + row) * kKv4Dim + d], o);
+        sum = fmaf(f, ml[w * mrows + row], sum);
       }
       const int r = row0 + row;
       if (whole) {
@@ -515,6 +603,12 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Args a) {
     __syncthreads();
     tile += hi - lo;
   }
+  // a warp that gave up has copies in flight: wait for them (again with a limit) before the memory is freed
+  if (!alive) {
+    const WaitGuard drain{&drain_mem, a.err, kWaitLimitNs};
+    for (; left_at < feed.issued; ++left_at)
+      if (!mbar_wait_warp(feed.bars + 8 * (left_at % kStages), (left_at / kStages) & 1u, drain)) break;
+  }
 }
 
 // ---------------------------------------------------------------- joining the parts
@@ -523,7 +617,9 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Args a) {
 template <int RPB>
 __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Args a, int ctas) {
   __shared__ int32_t prefix[kMaxBatch + 1];
+  pdl_launch_dependents();
   tile_prefix(a, prefix, false);
+  pdl_wait();
   const int64_t x = blockIdx.x;
   const int64_t bh = x / a.R;
   const int r = static_cast<int>(x - bh * a.R);
@@ -567,6 +663,7 @@ __global__ void __launch_bounds__(kThreads) kv4_weight_kernel(const Args a) {
   const int64_t bh = blockIdx.y;
   const int len = kv4_length(a.lengths[bh / a.H], a.cap, nullptr);
   const float* lse = a.row_lse + bh * a.R;
+  pdl_wait();
   for (int64_t slot = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; slot < len;
        slot += static_cast<int64_t>(gridDim.x) * kThreads) {
     float sum = 0.f;
@@ -582,14 +679,41 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
 int rows_of_block(int64_t R) { return R <= 8 ? 8 : 16; }
 
+// Launches a kernel that may start before its predecessor on the stream has
+// ended (it calls pdl_wait before it uses the predecessor's results).
+template <class... P, class... V>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t stream, V... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(kThreads);
+  c.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 template <int NT, bool kWeights>
 cudaError_t launch_main(const Args& a, int* ctas, cudaStream_t stream) {
+  static PerDeviceOnce once;
   int dev = 0, sms = 1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  *ctas = std::min(sms, kSmsMax) * (NT == 1 ? 4 : 3);
-  kv4_attn_kernel<NT, kWeights><<<*ctas, kThreads, 0, stream>>>(a);
+  const int64_t most = smem_bytes(8 * NT, 8 * NT, kMaxBatch);
+  e = once.run(dev, [&] {
+    return cudaFuncSetAttribute(kv4_attn_kernel<NT, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(most));
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t bytes = smem_bytes(a.R, 8 * NT, a.B);
+  // as many CTAs as an SM holds: registers allow 4 (3 with 16 rows), shared memory (1 KB a CTA is the system's) may
+  // allow fewer
+  const int64_t fit = 228 * 1024 / (bytes + 1024 + 256);
+  *ctas = std::min(sms, kSmsMax) * static_cast<int>(std::min<int64_t>(NT == 1 ? 4 : 3, fit));
+  kv4_attn_kernel<NT, kWeights><<<*ctas, kThreads, bytes, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -642,17 +766,14 @@ cudaError_t launch_kv4_attn(const Kv4AttnLaunch& p, cudaStream_t stream) {
     e = p.weight ? launch_main<2, true>(a, &ctas, stream) : launch_main<2, false>(a, &ctas, stream);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.B) * p.H * R;
-  if (rpb == 8)
-    kv4_join_kernel<8><<<static_cast<unsigned>(rows), kThreads, 0, stream>>>(a, ctas);
-  else
-    kv4_join_kernel<16><<<static_cast<unsigned>(rows), kThreads, 0, stream>>>(a, ctas);
-  e = cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(rows));
+  e = rpb == 8 ? launch_after(kv4_join_kernel<8>, grid, stream, a, ctas)
+               : launch_after(kv4_join_kernel<16>, grid, stream, a, ctas);
   if (e != cudaSuccess || !p.weight) return e;
   const int64_t pairs = static_cast<int64_t>(p.B) * p.H;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>((p.cap + kThreads - 1) / kThreads,
                                                               (8 * kSmsMax + pairs - 1) / pairs * 2));
-  kv4_weight_kernel<<<dim3(static_cast<unsigned>(want), static_cast<unsigned>(pairs)), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(kv4_weight_kernel, dim3(static_cast<unsigned>(want), static_cast<unsigned>(pairs)), stream, a);
 }
 
 }  // namespace ulysses
