@@ -42,6 +42,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "bounds.cuh"
 #include "internal.h"
@@ -366,17 +367,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
       }
     }
 
-    for (int tl = lo; tl < hi; ++tl) {
-      const int slot0 = tl * kTile + warp * kKv4BlockSlots;
-      if (slot0 >= len) break;
-      const uint32_t stage = used % kStages;
-      if (alive && !mbar_wait_warp(feed.bars + 8 * stage, (used / kStages) & 1u, guard)) {
-        alive = false;
-        left_at = used;
-      }
-      ++used;
-      const uint8_t* blk = ring + stage * kKv4BlockBytes;
-      const bool edge = slot0 + kKv4BlockSlots > lowest;
+    // One block of 32 slots at blk.  kEdge: some row does not see all of them.
+    auto step = [&](auto edge_tag, const uint8_t* blk, int slot0) {
+      constexpr bool kEdge = decltype(edge_tag)::value;
       uint4 meta[2][2];
       float s[NT][2][4];   // z log2 e: [16-slot half][slot g row 2t, g 2t+1, g+8 2t, g+8 2t+1]
 #pragma unroll
@@ -413,16 +406,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
             x = fmaf(bf16_hi(m.y), qsum[nt][row][1], x);
             x *= qscale[nt][row];
             const int slot = slot0 + 16 * mt + g + 8 * (c >> 1);
-            if (edge && slot >= limit[nt][row]) x = NEG_INF;
+            if (kEdge && slot >= limit[nt][row]) x = NEG_INF;
             s[nt][mt][c] = x;
             if (kWeights) {
               const int r = row0 + 8 * nt + 2 * t + row;
-              if (r < a.R && slot < len) a.logits[(bh * a.R + r) * a.cap + slot] = x;
+              if (r < a.R && (!kEdge || slot < len)) a.logits[(bh * a.R + r) * a.cap + slot] = x;
             }
           }
       }
       // slots behind the length hold anything: nothing of them may reach a sum
-      if (edge) {
+      if (kEdge) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -502,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
             w0[c] = p * (vs[mt][i][0] * s_up[0]);
             w1[c] = p * (vs[mt][i][1] * s_up[1]);
             float m0 = bf16_hi(m.z), m1 = bf16_hi(m.w);
-            if (edge && slot0 + 16 * mt + g + 8 * i >= limit[nt][row]) w0[c] = w1[c] = m0 = m1 = 0.f;
+            if (kEdge && slot0 + 16 * mt + g + 8 * i >= limit[nt][row]) w0[c] = w1[c] = m0 = m1 = 0.f;
             z0[nt][row][0] = fmaf(p, m0, z0[nt][row][0]);
             z0[nt][row][1] = fmaf(p, m1, z0[nt][row][1]);
           }
@@ -536,6 +529,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
             }
           }
       }
+    };
+
+    for (int tl = lo; tl < hi; ++tl) {
+      const int slot0 = tl * kTile + warp * kKv4BlockSlots;
+      if (slot0 >= len) break;
+      const uint32_t stage = used % kStages;
+      if (alive && !mbar_wait_warp(feed.bars + 8 * stage, (used / kStages) & 1u, guard)) {
+        alive = false;
+        left_at = used;
+      }
+      ++used;
+      const uint8_t* blk = ring + stage * kKv4BlockBytes;
+      if (slot0 + kKv4BlockSlots > lowest)
+        step(std::true_type{}, blk, slot0);
+      else
+        step(std::false_type{}, blk, slot0);
       __syncwarp();   // every lane has read the block before it is replaced
       if (alive) feed.next(a, prefix, warp, lane);
     }
