@@ -42,7 +42,7 @@ def test_sizes(B, H, cap):
     assert kv.cache_bytes == n * 152
     assert kv.workspace_bytes(H, 1) > 0
     extra = kv.workspace_bytes(2 * H, 3, True) - kv.workspace_bytes(2 * H, 3)
-    assert extra == (B * H * 6 * 4 + 255) // 256 * 256 + 4 * B * H * 6 * cap
+    assert 0 <= extra - 4 * B * H * 6 * cap < 8 * B * H * 6 + 256      # the logits, and a pair for each row
     assert kv.workspace_bytes(H + 1 if H > 1 else 0, 1) == 0
     assert kv.workspace_bytes(H, 0) == 0
 

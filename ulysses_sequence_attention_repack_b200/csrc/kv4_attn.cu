@@ -55,7 +55,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = 4;
 constexpr int kTile = kWarps * kKv4BlockSlots;   // slots of a tile
-constexpr int kMaxBatch = 1024;
 constexpr int kStages = 2;                       // blocks a warp has in flight
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
 constexpr int kSmsMax = 148;
@@ -74,7 +73,7 @@ struct Args {
   const int32_t* lengths;
   float* part_o;      // [2 * CTAs][rows of a block][128]: unfinished sums
   float2* part_ml;    // [2 * CTAs][rows of a block]: their maxima and sums of p
-  float* row_lse;     // [B * H][R]: log2 of the sums, for the weights
+  float2* row_ml;     // [B * H][R]: maxima and sums of rows that one CTA finished, for the weights
   float* logits;      // [B * H][R][cap]: z log2 e of the slots, for the weights
   int64_t cap, q_token_stride, q_head_stride;
   int32_t B, H, G, Lq, R, RB;
@@ -117,60 +116,80 @@ constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 
 // ---------------------------------------------------------------- the list of tiles
 
-// prefix[b] = tiles of the sequences before b, over all heads and row blocks.
-// Every thread of the block calls it.
-__device__ __forceinline__ void tile_prefix(const Args& a, int32_t* prefix, bool report) {
-  __shared__ int32_t sums[kThreads / 32];
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = threadIdx.x * per + i;
-    if (b < a.B) mine += (kv4_length(a.lengths[b], a.cap, report ? a.err : nullptr) + kTile - 1) / kTile;
-  }
-  int x = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) sums[w] = x;
-  __syncthreads();
-  int before = x - mine;
-  for (int i = 0; i < w; ++i) before += sums[i];
-  const int per_tile = a.H * a.RB;
-  for (int i = 0; i < per; ++i) {
-    const int b = threadIdx.x * per + i;
-    if (b >= a.B) break;
-    prefix[b] = before * per_tile;
-    before += (kv4_length(a.lengths[b], a.cap, nullptr) + kTile - 1) / kTile;
-    if (b == a.B - 1) prefix[a.B] = before * per_tile;
-  }
-  __syncthreads();
+// The list runs over sequences, then heads, then blocks of query rows, then
+// tiles.  Every warp finds its way by itself from the lengths, 32 at a time,
+// without a barrier: this is what a launch does before its first copy.
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// Tiles in the list.  report: flag lengths outside the cache.
+__device__ __forceinline__ int total_tiles(const Args& a, bool report) {
+  const int lane = threadIdx.x & 31;
+  unsigned int* err = report ? a.err : nullptr;
+  if (a.B == 1) return tiles_of(kv4_length(a.lengths[0], a.cap, lane == 0 ? err : nullptr)) * a.H * a.RB;
+  int n = 0;
+  for (int b = lane; b < a.B; b += 32) n += tiles_of(kv4_length(a.lengths[b], a.cap, err));
+  return __reduce_add_sync(0xffffffffu, n) * a.H * a.RB;
 }
 
-__device__ __forceinline__ int tiles_per_cta(int total, int ctas) { return (total + ctas - 1) / ctas; }
+// First tile of sequence b's in the list.
+__device__ __forceinline__ int first_tile(const Args& a, int b) {
+  if (b == 0) return 0;
+  int n = 0;
+  for (int i = threadIdx.x & 31; i < b; i += 32) n += tiles_of(kv4_length(a.lengths[i], a.cap, nullptr));
+  return __reduce_add_sync(0xffffffffu, n) * a.H * a.RB;
+}
 
-// A place in the list: tile `lo` of `ntiles` of one (sequence, head, row block).
+// A place in the list: tile `lo` of `ntiles` of unit (head, row block) `unit` of sequence b.
 struct Place {
   int b, len, ntiles, unit, lo;
 
-  __device__ __forceinline__ void find(const Args& a, const int32_t* prefix, int tile) {
-    int l = 0, h = a.B;   // prefix[l] <= tile < prefix[h], so the sequence found has tiles
-    while (h - l > 1) {
-      const int mid = (l + h) >> 1;
-      if (prefix[mid] <= tile)
-        l = mid;
-      else
-        h = mid;
+  // Tile number `tile`, below the total.
+  __device__ __forceinline__ void find(const Args& a, int tile) {
+    const int lane = threadIdx.x & 31, per = a.H * a.RB;
+    b = 0;
+    len = 0;
+    if (a.B == 1) {
+      len = kv4_length(a.lengths[0], a.cap, nullptr);
+    } else {
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int l = b0 + lane < a.B ? kv4_length(a.lengths[b0 + lane], a.cap, nullptr) : 0;
+        const int n = tiles_of(l) * per;
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, upto > tile);
+        if (past) {
+          const int at = __ffs(past) - 1;
+          b = b0 + at;
+          len = __shfl_sync(0xffffffffu, l, at);
+          tile -= __shfl_sync(0xffffffffu, upto - n, at);
+          break;
+        }
+        tile -= __shfl_sync(0xffffffffu, upto, 31);
+      }
     }
-    b = l;
-    len = kv4_length(a.lengths[b], a.cap, nullptr);
-    ntiles = (len + kTile - 1) / kTile;
-    unit = (tile - prefix[b]) / ntiles;
-    lo = (tile - prefix[b]) - unit * ntiles;
+    ntiles = tiles_of(len);
+    unit = tile / ntiles;
+    lo = tile - unit * ntiles;
+  }
+
+  // The first tile of the next unit; there is one.
+  __device__ __forceinline__ void next_unit(const Args& a) {
+    lo = 0;
+    if (++unit < a.H * a.RB) return;
+    unit = 0;
+    do {
+      len = ++b < a.B ? kv4_length(a.lengths[b], a.cap, nullptr) : 1;
+    } while (len == 0);
+    ntiles = tiles_of(len);
   }
 };
+
+__device__ __forceinline__ int tiles_per_cta(int total, int ctas) { return (total + ctas - 1) / ctas; }
 
 // The blocks that one warp takes of a CTA's run, copied ahead into its ring.
 struct Feed {
@@ -184,7 +203,7 @@ struct Feed {
   }
   // Starts the copy of the next block, if there is one.  A whole block is
   // copied even where the length ends inside it: it lies in the cache.
-  __device__ __forceinline__ void next(const Args& a, const int32_t* prefix, int warp, int lane) {
+  __device__ __forceinline__ void next(const Args& a, int warp, int lane) {
     while (tile < end) {
       const int block = at.lo * kWarps + warp;
       const bool exists = block * kKv4BlockSlots < at.len;
@@ -199,7 +218,7 @@ struct Feed {
       }
       ++tile;
       if (++at.lo == at.ntiles && tile < end) {
-        at.find(a, prefix, tile);
+        at.next_unit(a);
         locate(a);
       }
       if (exists) return;
@@ -207,13 +226,28 @@ struct Feed {
   }
 };
 
+// Row r of (sequence b, K/V head h): four dims a lane of the warp, from its sum
+// o, its sum of p and its maximum.
+__device__ __forceinline__ float row_log2(float sum, float M) { return sum == 0.f ? NEG_INF : M + log2f(sum); }
+
+__device__ __forceinline__ void finish_row(const Args& a, int b, int h, int r, int lane, float4 o, float sum, float M) {
+  const int i = r / a.G, hq = h * a.G + (r - i * a.G);
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  uint2 y;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.x) : "f"(o.y * f), "f"(o.x * f));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.y) : "f"(o.w * f), "f"(o.z * f));
+  const int64_t row = (static_cast<int64_t>(b) * a.Lq + i) * a.H * a.G + hq;
+  reinterpret_cast<uint2*>(a.out + row * kKv4Dim)[lane] = y;
+  if (a.lse && lane == 0) a.lse[(static_cast<int64_t>(b) * a.H * a.G + hq) * a.Lq + i] = row_log2(sum, M);
+}
+
 // ---------------------------------------------------------------- main kernel
 
 // Dynamic shared memory: the warps' rings, then their sums [warp][row][128],
-// maxima and sums of p [warp][row], then the prefix of tiles.
+// maxima and sums of p [warp][row].
 __host__ __device__ inline int smem_rows(int R, int RPB) { return R < RPB ? R : RPB; }
-__host__ __device__ inline int64_t smem_bytes(int R, int RPB, int B) {
-  return kWarps * (kStages * kKv4BlockBytes + smem_rows(R, RPB) * (kKv4Dim * 4 + 8)) + (B + 1) * 4;
+__host__ __device__ inline int64_t smem_bytes(int R, int RPB) {
+  return kWarps * (kStages * kKv4BlockBytes + smem_rows(R, RPB) * (kKv4Dim * 4 + 8));
 }
 
 template <int NT, bool kWeights>
@@ -229,7 +263,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
   float* mo = reinterpret_cast<float*>(smem + kWarps * kStages * kKv4BlockBytes);   // [warp][mrows][128]
   float* mM = mo + kWarps * mrows * kKv4Dim;
   float* ml = mM + kWarps * mrows;
-  int32_t* prefix = reinterpret_cast<int32_t*>(ml + kWarps * mrows);
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -237,9 +270,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
     for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bar_mem[0][0]) + 8 * i, 1);
     fence_mbar_init();
   }
-  tile_prefix(a, prefix, blockIdx.x == 0);   // (its barriers also order the initialisation above)
+  __syncthreads();
+  pdl_wait();
   const WaitGuard guard{&abort_mem, a.err, kWaitLimitNs};
-  const int total = prefix[a.B];
+  const int total = total_tiles(a, blockIdx.x == 0 && warp == 0);
   const int chunk = tiles_per_cta(total, gridDim.x);
   const int64_t first64 = static_cast<int64_t>(blockIdx.x) * chunk;
   if (first64 >= total) return;
@@ -247,8 +281,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
   const int tile_end = min(total, tile + chunk);
   const int run_begin = tile;
 
+  Place at;
+  at.find(a, tile);
   Feed feed;
-  feed.at.find(a, prefix, tile);
+  feed.at = at;
   feed.tile = tile;
   feed.end = tile_end;
   feed.locate(a);
@@ -256,15 +292,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
   feed.ring = smem_u32(ring);
   feed.bars = smem_u32(&bar_mem[warp][0]);
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) feed.next(a, prefix, warp, lane);
+  for (int i = 0; i < kStages; ++i) feed.next(a, warp, lane);
   uint32_t used = 0;        // blocks this warp has taken from its ring
   uint32_t left_at = 0;     // the block whose copy did not come
   bool alive = true;        // false once a wait has given up: nothing more is issued or waited for
 
   while (tile < tile_end) {
     // the fragment: tiles [lo, hi) of one (sequence, head, row block)
-    Place at;
-    at.find(a, prefix, tile);
     const int b = at.b, len = at.len, ntiles = at.ntiles, lo = at.lo;
     const int hi = min(ntiles, lo + tile_end - tile);
     const int h = at.unit / a.RB, rb = at.unit - h * a.RB;
@@ -546,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
       else
         step(std::false_type{}, blk, slot0);
       __syncwarp();   // every lane has read the block before it is replaced
-      if (alive) feed.next(a, prefix, warp, lane);
+      if (alive) feed.next(a, warp, lane);
     }
 
     // the fragment's sums: over the lanes that hold the same rows, then over the warps
@@ -578,39 +612,38 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
         }
       }
     __syncthreads();
+    // a warp takes every fourth row, a lane four of its dims
     const bool whole = lo == 0 && hi == ntiles;
     const int part = 2 * blockIdx.x + (tile == run_begin ? 0 : 1);
-    const int d = threadIdx.x;
-    for (int row = 0; row < RPB && row0 + row < a.R; ++row) {
+    for (int row = warp; row < RPB && row0 + row < a.R; row += kWarps) {
       float Mt = NEG_INF;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) Mt = fmaxf(Mt, mM[w * mrows + row]);
       const float base = Mt == NEG_INF ? 0.f : Mt;
-      float o = 0.f, sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2(mM[w * mrows + row] - base);
-        o = fmaf(f, mo[(w * mrows + row) * kKv4Dim + d], o);
+        const float4 x = reinterpret_cast<const float4*>(mo + (w * mrows + row) * kKv4Dim)[lane];
+        o.x = fmaf(f, x.x, o.x);
+        o.y = fmaf(f, x.y, o.y);
+        o.z = fmaf(f, x.z, o.z);
+        o.w = fmaf(f, x.w, o.w);
         sum = fmaf(f, ml[w * mrows + row], sum);
       }
       const int r = row0 + row;
       if (whole) {
-        const int i = r / a.G, hq = h * a.G + (r - i * a.G);
-        const float y = sum == 0.f ? 0.f : o / sum;
-        a.out[((static_cast<int64_t>(b) * a.Lq + i) * a.H * a.G + hq) * kKv4Dim + d] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(y));
-        if (d == 0) {
-          const float ls = sum == 0.f ? NEG_INF : Mt + log2f(sum);
-          if (a.lse) a.lse[(static_cast<int64_t>(b) * a.H * a.G + hq) * a.Lq + i] = ls;
-          if (kWeights) a.row_lse[bh * a.R + r] = ls;
-        }
+        finish_row(a, b, h, r, lane, o, sum, Mt);
+        if (kWeights && lane == 0) a.row_ml[bh * a.R + r] = make_float2(Mt, sum);
       } else {
-        a.part_o[(static_cast<int64_t>(part) * RPB + row) * kKv4Dim + d] = o;
-        if (d == 0) a.part_ml[part * RPB + row] = make_float2(Mt, sum);
+        reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(part) * RPB + row) * kKv4Dim)[lane] = o;
+        if (lane == 0) a.part_ml[part * RPB + row] = make_float2(Mt, sum);
       }
     }
     __syncthreads();
     tile += hi - lo;
+    if (tile < tile_end) at.next_unit(a);
   }
   // a warp that gave up has copies in flight: wait for them (again with a limit) before the memory is freed
   if (!alive) {
@@ -622,65 +655,135 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(con
 
 // ---------------------------------------------------------------- joining the parts
 
-// One block per row.  A row whose tiles one CTA held is done already.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kWeightSlots = kJoinThreads * 4;   // slots of a block that adds weights
+
+// The parts that one unit's tiles were cut into: those of CTAs c0 .. c1.  A
+// unit that one CTA held is whole.
+struct Parts {
+  int c0, c1, chunk, t0;
+  __device__ __forceinline__ void find(const Args& a, int ctas, int b, int unit, int ntiles) {
+    chunk = tiles_per_cta(total_tiles(a, false), ctas);
+    t0 = first_tile(a, b) + unit * ntiles;
+    c0 = t0 / chunk;
+    c1 = (t0 + ntiles - 1) / chunk;
+  }
+  // a CTA's run begins with this unit, or it is the run's last
+  __device__ __forceinline__ int part(int c) const { return 2 * c + (c * chunk >= t0 ? 0 : 1); }
+};
+
+// One warp: the maximum over the parts of a row, and the sum of p for it.
 template <int RPB>
-__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Args a, int ctas) {
-  __shared__ int32_t prefix[kMaxBatch + 1];
-  pdl_launch_dependents();
-  tile_prefix(a, prefix, false);
-  pdl_wait();
-  const int64_t x = blockIdx.x;
-  const int64_t bh = x / a.R;
-  const int r = static_cast<int>(x - bh * a.R);
-  const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
-  const int rb = r / RPB, row = r - rb * RPB;
-  const int d = threadIdx.x;
-  const int i = r / a.G, hq = h * a.G + (r - i * a.G);
-  const int64_t at = ((static_cast<int64_t>(b) * a.Lq + i) * a.H * a.G + hq) * kKv4Dim + d;
-  const int64_t lse_at = (static_cast<int64_t>(b) * a.H * a.G + hq) * a.Lq + i;
-  const int len = kv4_length(a.lengths[b], a.cap, nullptr);
-  const int ntiles = (len + kTile - 1) / kTile;
-  float o = 0.f, sum = 0.f, Mt = NEG_INF;
-  if (ntiles > 0) {
-    const int chunk = tiles_per_cta(prefix[a.B], ctas);
-    const int t0 = prefix[b] + (h * a.RB + rb) * ntiles, t1 = t0 + ntiles;
-    const int c0 = t0 / chunk, c1 = (t1 - 1) / chunk;
-    if (c0 == c1) return;
-    for (int c = c0; c <= c1; ++c) {
-      const int part = 2 * c + (c * chunk >= t0 ? 0 : 1);
-      Mt = fmaxf(Mt, a.part_ml[part * RPB + row].x);
-    }
-    const float base = Mt == NEG_INF ? 0.f : Mt;
-    for (int c = c0; c <= c1; ++c) {
-      const int part = 2 * c + (c * chunk >= t0 ? 0 : 1);
-      const float2 m = a.part_ml[part * RPB + row];
-      const float f = ex2(m.x - base);
-      o = fmaf(f, a.part_o[(static_cast<int64_t>(part) * RPB + row) * kKv4Dim + d], o);
-      sum = fmaf(f, m.y, sum);
-    }
+__device__ __forceinline__ float2 join_ml(const Args& a, const Parts& p, int row) {
+  const int lane = threadIdx.x & 31;
+  float M = NEG_INF, sum = 0.f;
+  for (int c = p.c0 + lane; c <= p.c1; c += 32) {
+    const float2 x = a.part_ml[p.part(c) * RPB + row];
+    const float m = fmaxf(M, x.x);
+    const float base = m == NEG_INF ? 0.f : m;
+    sum = sum * ex2(M - base) + x.y * ex2(x.x - base);
+    M = m;
   }
-  a.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o / sum));
-  if (d == 0) {
-    const float ls = sum == 0.f ? NEG_INF : Mt + log2f(sum);
-    if (a.lse) a.lse[lse_at] = ls;
-    if (a.row_lse) a.row_lse[bh * a.R + r] = ls;
-  }
+  float top = M;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  sum *= ex2(M - (top == NEG_INF ? 0.f : top));
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return make_float2(top, sum);
 }
 
-// weight_t += sum_r 2^(z_rt - lse_r), the rows in their order.
-__global__ void __launch_bounds__(kThreads) kv4_weight_kernel(const Args a) {
-  const int64_t bh = blockIdx.y;
-  const int len = kv4_length(a.lengths[bh / a.H], a.cap, nullptr);
-  const float* lse = a.row_lse + bh * a.R;
+// Blocks below `rows`: one row each, whose parts the warps share.  Further
+// blocks: kWeightSlots slots of a pair each, weight_t += sum_r 2^(z_rt - lse_r),
+// the rows in their order.
+template <int RPB>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, int ctas, int64_t rows) {
+  __shared__ __align__(16) float so[kJoinWarps][kKv4Dim];
+  __shared__ float slse[64];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
   pdl_wait();
-  for (int64_t slot = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; slot < len;
-       slot += static_cast<int64_t>(gridDim.x) * kThreads) {
-    float sum = 0.f;
-    for (int r = 0; r < a.R; ++r) {
-      const float x = lse[r];
-      if (x != NEG_INF) sum += ex2(a.logits[(bh * a.R + r) * a.cap + slot] - x);
+  const int64_t x = blockIdx.x;
+  if (x < rows) {
+    const int64_t bh = x / a.R;
+    const int r = static_cast<int>(x - bh * a.R);
+    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+    const int row = r % RPB;
+    const int ntiles = tiles_of(kv4_length(a.lengths[b], a.cap, nullptr));
+    if (ntiles == 0) {
+      if (warp == 0) finish_row(a, b, h, r, lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, NEG_INF);
+      return;
     }
-    a.weight[bh * a.cap + slot] += sum;
+    Parts p;
+    p.find(a, ctas, b, h * a.RB + r / RPB, ntiles);
+    if (p.c0 == p.c1) return;
+    const float2 ml = join_ml<RPB>(a, p, row);
+    const float base = ml.x == NEG_INF ? 0.f : ml.x;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = p.c0 + warp; c <= p.c1; c += kJoinWarps) {
+      const int64_t at = static_cast<int64_t>(p.part(c)) * RPB + row;
+      const float f = ex2(a.part_ml[at].x - base);
+      const float4 y = reinterpret_cast<const float4*>(a.part_o + at * kKv4Dim)[lane];
+      o.x = fmaf(f, y.x, o.x);
+      o.y = fmaf(f, y.y, o.y);
+      o.z = fmaf(f, y.z, o.z);
+      o.w = fmaf(f, y.w, o.w);
+    }
+    reinterpret_cast<float4*>(so[warp])[lane] = o;
+    __syncthreads();
+    if (warp) return;
+    const int n = min(kJoinWarps, p.c1 - p.c0 + 1);
+    for (int w = 1; w < n; ++w) {
+      const float4 y = reinterpret_cast<const float4*>(so[w])[lane];
+      o.x += y.x;
+      o.y += y.y;
+      o.z += y.z;
+      o.w += y.w;
+    }
+    finish_row(a, b, h, r, lane, o, ml.y, ml.x);
+    return;
+  }
+  const int64_t per = (a.cap + kWeightSlots - 1) / kWeightSlots, y = x - rows;
+  const int64_t bh = y / per;
+  const int64_t slot = (y - bh * per) * kWeightSlots + threadIdx.x * 4;
+  const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+  const int len = kv4_length(a.lengths[b], a.cap, nullptr);
+  if ((y - bh * per) * kWeightSlots >= len) return;
+  const int ntiles = tiles_of(len);
+  float4* w = reinterpret_cast<float4*>(a.weight + bh * a.cap + slot);   // capacities are multiples of 32
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r0 = 0; r0 < a.R; r0 += 64) {
+    for (int r = r0 + warp; r < min(a.R, r0 + 64); r += kJoinWarps) {
+      Parts p;
+      p.find(a, ctas, b, h * a.RB + r / RPB, ntiles);
+      const float2 ml = p.c0 == p.c1 ? a.row_ml[bh * a.R + r] : join_ml<RPB>(a, p, r % RPB);
+      if (lane == 0) slse[r - r0] = row_log2(ml.y, ml.x);
+    }
+    __syncthreads();
+    if (slot < len) {
+#pragma unroll 4
+      for (int r = r0; r < min(a.R, r0 + 64); ++r) {
+        const float lse = slse[r - r0];
+        const float4 z = *reinterpret_cast<const float4*>(a.logits + (bh * a.R + r) * a.cap + slot);
+        if (lse == NEG_INF) continue;
+        sum.x += ex2(z.x - lse);
+        sum.y += ex2(z.y - lse);
+        sum.z += ex2(z.z - lse);
+        sum.w += ex2(z.w - lse);
+      }
+    }
+    __syncthreads();
+  }
+  if (slot + 3 < len) {
+    const float4 v = *w;
+    *w = make_float4(v.x + sum.x, v.y + sum.y, v.z + sum.z, v.w + sum.w);
+  } else if (slot < len) {   // the slots behind the length keep what they hold
+    float* f = reinterpret_cast<float*>(w);
+    f[0] += sum.x;
+    if (slot + 1 < len) f[1] += sum.y;
+    if (slot + 2 < len) f[2] += sum.z;
   }
 }
 
@@ -691,10 +794,13 @@ int rows_of_block(int64_t R) { return R <= 8 ? 8 : 16; }
 // Launches a kernel that may start before its predecessor on the stream has
 // ended (it calls pdl_wait before it uses the predecessor's results).
 template <class... P, class... V>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t stream, V... args) {
+cudaError_t launch_after(void (*kernel)(P...), int64_t grid, int threads, int64_t smem, cudaStream_t stream,
+                         V... args) {
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t c = {};
-  c.gridDim = grid;
-  c.blockDim = dim3(kThreads);
+  c.gridDim = dim3(static_cast<unsigned>(grid));
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = static_cast<size_t>(smem);
   c.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -711,19 +817,18 @@ cudaError_t launch_main(const Args& a, int* ctas, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t most = smem_bytes(8 * NT, 8 * NT, kMaxBatch);
+  const int64_t most = smem_bytes(8 * NT, 8 * NT);
   e = once.run(dev, [&] {
     return cudaFuncSetAttribute(kv4_attn_kernel<NT, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(most));
   });
   if (e != cudaSuccess) return e;
-  const int64_t bytes = smem_bytes(a.R, 8 * NT, a.B);
+  const int64_t bytes = smem_bytes(a.R, 8 * NT);
   // as many CTAs as an SM holds: registers allow 4 (3 with 16 rows), shared memory (1 KB a CTA is the system's) may
   // allow fewer
   const int64_t fit = 228 * 1024 / (bytes + 1024 + 256);
   *ctas = std::min(sms, kSmsMax) * static_cast<int>(std::min<int64_t>(NT == 1 ? 4 : 3, fit));
-  kv4_attn_kernel<NT, kWeights><<<*ctas, kThreads, bytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(kv4_attn_kernel<NT, kWeights>, *ctas, kThreads, bytes, stream, a);
 }
 
 }  // namespace
@@ -733,7 +838,7 @@ cudaError_t launch_main(const Args& a, int* ctas, cudaStream_t stream) {
 int64_t kv4_attn_workspace_bytes(int32_t B, int32_t H, int32_t G, int32_t Lq, int64_t cap, bool weights) {
   const int64_t R = static_cast<int64_t>(G) * Lq, rpb = rows_of_block(R);
   int64_t n = up256(2 * kMaxCtas * rpb * kKv4Dim * 4) + up256(2 * kMaxCtas * rpb * 8);
-  if (weights) n += up256(static_cast<int64_t>(B) * H * R * 4) + static_cast<int64_t>(B) * H * R * cap * 4;
+  if (weights) n += up256(static_cast<int64_t>(B) * H * R * 8) + static_cast<int64_t>(B) * H * R * cap * 4;
   return n;
 }
 
@@ -752,8 +857,8 @@ cudaError_t launch_kv4_attn(const Kv4AttnLaunch& p, cudaStream_t stream) {
   w += up256(static_cast<int64_t>(2) * kMaxCtas * rpb * kKv4Dim * 4);
   a.part_ml = reinterpret_cast<float2*>(w);
   w += up256(static_cast<int64_t>(2) * kMaxCtas * rpb * 8);
-  a.row_lse = p.weight ? reinterpret_cast<float*>(w) : nullptr;
-  w += up256(static_cast<int64_t>(p.B) * p.H * R * 4);
+  a.row_ml = p.weight ? reinterpret_cast<float2*>(w) : nullptr;
+  w += up256(static_cast<int64_t>(p.B) * p.H * R * 8);
   a.logits = p.weight ? reinterpret_cast<float*>(w) : nullptr;
   a.cap = p.cap;
   a.q_token_stride = p.q_token_stride;
@@ -775,14 +880,10 @@ cudaError_t launch_kv4_attn(const Kv4AttnLaunch& p, cudaStream_t stream) {
     e = p.weight ? launch_main<2, true>(a, &ctas, stream) : launch_main<2, false>(a, &ctas, stream);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.B) * p.H * R;
-  const dim3 grid(static_cast<unsigned>(rows));
-  e = rpb == 8 ? launch_after(kv4_join_kernel<8>, grid, stream, a, ctas)
-               : launch_after(kv4_join_kernel<16>, grid, stream, a, ctas);
-  if (e != cudaSuccess || !p.weight) return e;
-  const int64_t pairs = static_cast<int64_t>(p.B) * p.H;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((p.cap + kThreads - 1) / kThreads,
-                                                              (8 * kSmsMax + pairs - 1) / pairs * 2));
-  return launch_after(kv4_weight_kernel, dim3(static_cast<unsigned>(want), static_cast<unsigned>(pairs)), stream, a);
+  const int64_t weight_blocks =
+      p.weight ? static_cast<int64_t>(p.B) * p.H * ((p.cap + kWeightSlots - 1) / kWeightSlots) : 0;
+  return rpb == 8 ? launch_after(kv4_join_kernel<8>, rows + weight_blocks, kJoinThreads, 0, stream, a, ctas, rows)
+                  : launch_after(kv4_join_kernel<16>, rows + weight_blocks, kJoinThreads, 0, stream, a, ctas, rows);
 }
 
 }  // namespace ulysses
