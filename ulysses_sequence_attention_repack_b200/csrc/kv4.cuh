@@ -28,6 +28,7 @@
 // capacity], token positions int32 [batch, heads, capacity].
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -56,6 +57,27 @@ __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u 
 // results before pdl_wait().
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launches a kernel that may start before its predecessor on the stream has
+// ended (it calls pdl_wait before it touches global memory), in clusters of
+// `cluster` blocks.
+template <class... P, class... V>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int64_t smem, int cluster, cudaStream_t stream,
+                         V... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = static_cast<size_t>(smem);
+  c.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  c.attrs = at;
+  c.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
 
 // A device-side length, held inside 0 .. capacity (and reported if it was not).
 __device__ __forceinline__ int kv4_length(int n, int64_t capacity, unsigned int* err) {

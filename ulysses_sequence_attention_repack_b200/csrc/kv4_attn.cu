@@ -58,7 +58,7 @@ constexpr int kTile = kWarps * kKv4BlockSlots;   // slots of a tile
 constexpr int kStages = 2;                       // blocks a warp has in flight
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
 constexpr int kSmsMax = 148;
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = kSmsMax * kCtasPerSm;   // sizes the workspace; the grid never passes it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;                     // log2 by which a maximum may be passed before it moves
@@ -251,7 +251,7 @@ __host__ __device__ inline int64_t smem_bytes(int R, int RPB) {
 }
 
 template <int NT, bool kWeights>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_attn_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(const Args a) {
   constexpr int RPB = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bar_mem[kWarps][kStages];
@@ -791,25 +791,6 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
 int rows_of_block(int64_t R) { return R <= 8 ? 8 : 16; }
 
-// Launches a kernel that may start before its predecessor on the stream has
-// ended (it calls pdl_wait before it uses the predecessor's results).
-template <class... P, class... V>
-cudaError_t launch_after(void (*kernel)(P...), int64_t grid, int threads, int64_t smem, cudaStream_t stream,
-                         V... args) {
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(static_cast<unsigned>(grid));
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = static_cast<size_t>(smem);
-  c.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, args...);
-}
-
 template <int NT, bool kWeights>
 cudaError_t launch_main(const Args& a, int* ctas, cudaStream_t stream) {
   static PerDeviceOnce once;
@@ -824,11 +805,11 @@ cudaError_t launch_main(const Args& a, int* ctas, cudaStream_t stream) {
   });
   if (e != cudaSuccess) return e;
   const int64_t bytes = smem_bytes(a.R, 8 * NT);
-  // as many CTAs as an SM holds: registers allow 4 (3 with 16 rows), shared memory (1 KB a CTA is the system's) may
+  // as many CTAs as an SM holds: registers allow 3 (2 with 16 rows), shared memory (1 KB a CTA is the system's) may
   // allow fewer
   const int64_t fit = 228 * 1024 / (bytes + 1024 + 256);
-  *ctas = std::min(sms, kSmsMax) * static_cast<int>(std::min<int64_t>(NT == 1 ? 4 : 3, fit));
-  return launch_after(kv4_attn_kernel<NT, kWeights>, *ctas, kThreads, bytes, stream, a);
+  *ctas = std::min(sms, kSmsMax) * static_cast<int>(std::min<int64_t>(NT == 1 ? 3 : 2, fit));
+  return launch_after(kv4_attn_kernel<NT, kWeights>, dim3(*ctas), kThreads, bytes, 1, stream, a);
 }
 
 }  // namespace
@@ -882,8 +863,10 @@ cudaError_t launch_kv4_attn(const Kv4AttnLaunch& p, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.H * R;
   const int64_t weight_blocks =
       p.weight ? static_cast<int64_t>(p.B) * p.H * ((p.cap + kWeightSlots - 1) / kWeightSlots) : 0;
-  return rpb == 8 ? launch_after(kv4_join_kernel<8>, rows + weight_blocks, kJoinThreads, 0, stream, a, ctas, rows)
-                  : launch_after(kv4_join_kernel<16>, rows + weight_blocks, kJoinThreads, 0, stream, a, ctas, rows);
+  if (rows + weight_blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(rows + weight_blocks));
+  return rpb == 8 ? launch_after(kv4_join_kernel<8>, grid, kJoinThreads, 0, 1, stream, a, ctas, rows)
+                  : launch_after(kv4_join_kernel<16>, grid, kJoinThreads, 0, 1, stream, a, ctas, rows);
 }
 
 }  // namespace ulysses
