@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTokens = 8;   // consecutive tokens of one head a warp has in flight
+constexpr int kRun = 8;   // consecutive tokens of one head a warp takes together
 
 __device__ __forceinline__ int4 ld_stream(const int4* p) {
   int4 v;
@@ -29,8 +29,8 @@ __device__ __forceinline__ int4 ld_stream(const int4* p) {
   return v;
 }
 
-// Where rows i0 .. i0 + 7 live: lane u < 8 gets the pair (sequence, slot) of
-// row i0 + u, slot -1 for a row of no sequence or a slot outside the cache.
+// Where row i0 + lane lives, for lanes below T: its sequence and slot; slot -1
+// for a row of no sequence or a slot outside the cache.
 struct RowPlace {
   int b;
   int64_t slot;
@@ -40,6 +40,7 @@ struct RowPlace {
 // warp looks for i0's sequence, 32 entries a round (one round below 32
 // sequences), then counts the ends that rows i0 + 1 .. pass.  cu is read inside
 // [0, batch] only, whatever it holds.
+template <int T>
 __device__ __forceinline__ RowPlace place_rows(const Kv4Rows& r, int64_t i0, int batch, int64_t capacity,
                                                unsigned int* err) {
   const int lane = threadIdx.x & 31;
@@ -51,16 +52,18 @@ __device__ __forceinline__ RowPlace place_rows(const Kv4Rows& r, int64_t i0, int
     hi = min(hi, lo + step - 1);
   }
   const int b0 = lo + __popc(__ballot_sync(0xffffffffu, lo + lane <= hi && r.cu[min(lo + lane, hi)] <= i0)) - 1;
-  const int64_t end = b0 + 1 + lane <= batch ? r.cu[b0 + 1 + lane] : INT64_MAX;
   int b = b0;
+  if (T > 1) {
+    const int64_t end = b0 + 1 + lane <= batch ? r.cu[b0 + 1 + lane] : INT64_MAX;
 #pragma unroll
-  for (int u = 1; u < kTokens; ++u) {
-    const int n = __popc(__ballot_sync(0xffffffffu, end <= i0 + u));
-    if (lane == u) b = b0 + n;
+    for (int u = 1; u < T; ++u) {
+      const int n = __popc(__ballot_sync(0xffffffffu, end <= i0 + u));
+      if (lane == u) b = b0 + n;
+    }
   }
   const int64_t i = i0 + lane;
   RowPlace p{0, -1};
-  if (lane >= kTokens || i >= r.rows || b < 0 || b >= batch) return p;
+  if (lane >= T || i >= r.rows || b < 0 || b >= batch) return p;
   if (b == b0 + 32)   // many empty sequences in a row: go on one by one
     while (b < batch && r.cu[b + 1] <= i) ++b;
   if (b >= batch) return p;
@@ -73,6 +76,23 @@ __device__ __forceinline__ RowPlace place_rows(const Kv4Rows& r, int64_t i0, int
     p.slot = -1;
   }
   return p;
+}
+
+// Whether rows i0 .. i0 + T - 1 fill consecutive slots of one sequence.
+template <int T>
+__device__ __forceinline__ bool one_run(const RowPlace& p) {
+  if (T == 1) return __shfl_sync(0xffffffffu, p.slot, 0) >= 0;
+  const int lane = threadIdx.x & 31;
+  const int b = __shfl_sync(0xffffffffu, p.b, 0);
+  const int64_t slot = __shfl_sync(0xffffffffu, p.slot, 0);
+  return __all_sync(0xffffffffu, lane >= T || (slot >= 0 && p.b == b && p.slot == slot + lane));
+}
+
+// Offset of the slot `at` slots on from the start of a block: from its code
+// row and its scales.  (at < 64: in this block or the pair's next.)
+__device__ __forceinline__ int code_row(int at) { return at * 64 + (at >> 5) * (kKv4BlockBytes - 32 * 64); }
+__device__ __forceinline__ int meta_row(int at) {
+  return kKv4MetaOffset + at * 16 + (at >> 5) * (kKv4BlockBytes - 32 * 16);
 }
 
 __device__ __forceinline__ int64_t row_offset(const Kv4Rows& r, int64_t i, int h) {
@@ -101,178 +121,219 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// The code of d = x - m >= 0 for a step s, by a division: for steps so small
-// that their reciprocal is not a number to work with.
-__device__ __noinline__ uint32_t code_by_division(float d, float s) {
-  return static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(d, s)), 0.f), 15.f));
+// Value e of 16, given as bf16 pairs.
+__device__ __forceinline__ float value_of(const uint32_t (&w)[8], int e) {
+  return e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
 }
 
-// Append: one warp takes 8 consecutive tokens of one head (neighbouring warps
-// the neighbouring heads, whose rows are neighbours in memory).  Half a warp
-// holds a row, 8 dims a lane: lanes 0-15 the K row, 16-31 the V row, so a
-// group of 64 is 8 lanes and its minimum and maximum three shuffles of pairs.
+// Codes by divisions: for steps so small that their reciprocal is not a number
+// to work with.
+__device__ __noinline__ uint2 codes_by_division(uint4 w0, uint4 w1, float lo, float s) {
+  const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+  uint2 code = make_uint2(0, 0);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float n = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(value_of(w, e), lo), s)), 0.f), 15.f);
+    (e < 8 ? code.x : code.y) |= static_cast<uint32_t>(n) << (4 * (e & 7));
+  }
+  return code;
+}
+
+// The codes of this lane's 16 values of a group, whose other values the lanes
+// of its quad hold; *meta gets the group's step and minimum.
 //
 // n = round((x - m) / s) without a division: t = d r rounded to an integer by
 // adding 1.5 2^23 (r an approximate 1 / s) is the right integer or, next to a
-// border, its neighbour.  The residual d - n s is exact (d and s are bf16
-// differences and steps: |d - n s| <= s is a multiple of d's last place), so
-// comparing it with s / 2 tells which, and finds the ties, which go to even.
+// border, its neighbour.  The residual d - n s is exact (|d - n s| <= s is a
+// multiple of d's last place and of s's), so comparing it with s / 2 tells
+// which, and finds the ties, which go to even.  About one value in 300 of
+// bf16 data is such a tie; they are put right one after another.
+__device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* meta) {
+  uint32_t lo2 = w[0], hi2 = w[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    lo2 = min2(lo2, w[i]);
+    hi2 = max2(hi2, w[i]);
+  }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    lo2 = min2(lo2, __shfl_xor_sync(0xffffffffu, lo2, d));
+    hi2 = max2(hi2, __shfl_xor_sync(0xffffffffu, hi2, d));
+  }
+  const float lo = min_nan(bf16_lo(lo2), bf16_hi(lo2)), hi = max_nan(bf16_lo(hi2), bf16_hi(hi2));
+  // (hi - lo) / 15 by its reciprocal and one correction, which is exact where the quotient is a bf16 border
+  const float spread = __fsub_rn(hi, lo);
+  const float q0 = spread * (1.0f / 15.0f);
+  const float s = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-q0, 15.0f, spread), 1.0f / 15.0f, q0)));
+  const bool finite = fabsf(s) <= 3.4e38f && fabsf(lo) <= 3.4e38f;
+  *meta = finite ? (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u) : 0x7fc07fc0u;
+  if (!(finite && s > 0.f)) return make_uint2(0, 0);
+  if (s < 0x1p-100f)
+    return codes_by_division(make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]), lo, s);
+  constexpr float kRound = 12582912.f;   // 1.5 2^23, bits 0x4B400000
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  const float half = 0.5f * s;
+  uint32_t off = 0;   // bit e: value e lies half a step or more from its code
+  uint32_t code[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    code[j] = 0u - (0x4B400000u + 0xB4000000u + 0x40000000u);   // less the sum of 0x4B400000 << 4 e
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = __fsub_rn(value_of(w, 8 * j + e), lo);
+      const float t = fmaf(d, r, kRound);
+      if (fabsf(fmaf(-(t - kRound), s, d)) >= half) off |= 1u << (8 * j + e);
+      code[j] += __float_as_uint(t) * (1u << (4 * e));
+    }
+  }
+  while (off) {
+    const int e = __ffs(off) - 1, at = 4 * (e & 7);
+    off &= off - 1;
+    uint32_t u = 0, c = e < 8 ? code[0] : code[1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u = (e >> 1) == i ? w[i] : u;
+    const uint32_t n = (c >> at) & 15u;
+    const float rest = fmaf(-static_cast<float>(n), s, __fsub_rn(e & 1 ? bf16_hi(u) : bf16_lo(u), lo));
+    // past the border, or on it and odd: one step towards the value
+    if (fabsf(rest) > half || (n & 1u)) c += rest > 0.f ? 1u << at : 0u - (1u << at);
+    if (e < 8)
+      code[0] = c;
+    else
+      code[1] = c;
+  }
+  return make_uint2(code[0], code[1]);
+}
+
+// Append: one warp takes 8 consecutive tokens of one head (neighbouring warps
+// the neighbouring heads, whose rows are neighbours in memory), their K rows
+// and then their V rows.  Four lanes hold a row, 16 values of each group a
+// lane: few lanes a group make its minimum and maximum cheap (two shuffles),
+// and with 8 dims a lane the kernel spent twice the instructions, 295 us for
+// 19,394 tokens x 56 heads.  A lane's token has a place of its own, so tokens
+// of many sequences (a decoding step) go side by side.
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowsLaunch a) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t groups = (a.r.rows + kTokens - 1) / kTokens;
+  const int64_t groups = (a.r.rows + kRun - 1) / kRun;
   pdl_wait();
   if (item >= groups * a.H) return;
-  const int64_t i0 = item / a.H * kTokens;
+  const int64_t i0 = item / a.H * kRun;
   const int h = static_cast<int>(item - item / a.H * a.H);
-  const int plane = lane >> 4, l16 = lane & 15;
-  const uint16_t* src = static_cast<const uint16_t*>(plane ? a.r.v : a.r.k) + row_offset(a.r, i0, h) + l16 * 8;
-  int4 x[kTokens];
+  const int u = lane >> 2, q = lane & 3;   // token; which 8 of every 32 dims
+  const int64_t row = row_offset(a.r, i0 + u, h) + q * 8;
+  uint4 x[2][4];
 #pragma unroll
-  for (int u = 0; u < kTokens; ++u) {
-    x[u] = make_int4(0, 0, 0, 0);
-    if (i0 + u < a.r.rows) x[u] = ld_stream(reinterpret_cast<const int4*>(src + u * a.r.token_stride));
-  }
-  const RowPlace mine = place_rows(a.r, i0, a.B, a.cap, a.err);
-  uint32_t meta[kTokens];
+  for (int plane = 0; plane < 2; ++plane)
 #pragma unroll
-  for (int u = 0; u < kTokens; ++u) {
-    const int64_t slot = __shfl_sync(0xffffffffu, mine.slot, u);
-    const int64_t bh = static_cast<int64_t>(__shfl_sync(0xffffffffu, mine.b, u)) * a.H + h;
-    const uint32_t w[4] = {static_cast<uint32_t>(x[u].x), static_cast<uint32_t>(x[u].y),
-                           static_cast<uint32_t>(x[u].z), static_cast<uint32_t>(x[u].w)};
-    uint32_t lo2 = min2(min2(w[0], w[1]), min2(w[2], w[3])), hi2 = max2(max2(w[0], w[1]), max2(w[2], w[3]));
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) {
-      lo2 = min2(lo2, __shfl_xor_sync(0xffffffffu, lo2, d));
-      hi2 = max2(hi2, __shfl_xor_sync(0xffffffffu, hi2, d));
-    }
-    const float lo = min_nan(bf16_lo(lo2), bf16_hi(lo2)), hi = max_nan(bf16_lo(hi2), bf16_hi(hi2));
-    // (hi - lo) / 15 by its reciprocal and one correction, which is exact where the quotient is a bf16 border
-    const float spread = __fsub_rn(hi, lo);
-    const float q0 = spread * (1.0f / 15.0f);
-    const float s = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-q0, 15.0f, spread), 1.0f / 15.0f, q0)));
-    const bool finite = fabsf(s) <= 3.4e38f && fabsf(lo) <= 3.4e38f;
-    uint32_t code = 0;
-    if (finite && s > 0.f) {
-      if (s < 0x1p-100f) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          code |= code_by_division(__fsub_rn(e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]), lo), s) << (4 * e);
-      } else {
-        constexpr float kRound = 12582912.f;   // 1.5 2^23, bits 0x4B400000
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-        const float half = 0.5f * s;
-        bool border = false;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = __fsub_rn(e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]), lo);
-          const float t = fmaf(d, r, kRound);
-          border |= fabsf(fmaf(-(t - kRound), s, d)) >= half;
-          code += __float_as_uint(t) << (4 * e);
-        }
-        // (each t's upper bits: the sum of 0x4B400000 << 4 e)
-        constexpr uint32_t kExtra = 0x4B400000u + 0xB4000000u + 0x40000000u;
-        code -= kExtra;
-        if (border) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float d = __fsub_rn(e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]), lo);
-            const uint32_t n = (code >> (4 * e)) & 15u;
-            const float rest = fmaf(-static_cast<float>(n), s, d);
-            // one step on or back past the border; on it, to the even one
-            if (rest > half || (rest == half && (n & 1u))) code += 1u << (4 * e);
-            if (rest < -half || (rest == -half && (n & 1u))) code -= 1u << (4 * e);
-          }
-        }
+    for (int i = 0; i < 4; ++i) {
+      x[plane][i] = make_uint4(0, 0, 0, 0);
+      if (i0 + u < a.r.rows) {
+        const int4 v = ld_stream(reinterpret_cast<const int4*>(static_cast<const uint16_t*>(plane ? a.r.v : a.r.k) +
+                                                               row + 32 * i));
+        x[plane][i] = make_uint4(v.x, v.y, v.z, v.w);
       }
     }
-    meta[u] = finite ? (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u) : 0x7fc07fc0u;
-    if (slot < 0) continue;
-    const int64_t c_off = kv4_block_offset(bh, a.cap, slot) + plane * kKv4VOffset +
-                          static_cast<int>(slot % kKv4BlockSlots) * 64 + (l16 & 7) * 8 + (l16 >> 3) * 4;
-    if (in_bounds(c_off, 4, a.blocks_bytes, a.err)) *reinterpret_cast<uint32_t*>(a.cache + c_off) = code;
-  }
-  // Scales, weights and positions of the 8 tokens in one store each: lane
-  // 4 u + p writes part p of token u's scales, lane u its weight and position.
-  {
-    const int u = lane >> 2, p = lane & 3;
-    uint32_t m = 0;
+  const RowPlace mine = place_rows<kRun>(a.r, i0, a.B, a.cap, a.err);
+  const int64_t slot = __shfl_sync(0xffffffffu, mine.slot, u);
+  const int b = __shfl_sync(0xffffffffu, mine.b, u);
+  const int64_t bh = static_cast<int64_t>(b) * a.H + h;
+  const int64_t blk = kv4_block_offset(bh, a.cap, max(slot, int64_t(0)));
+  const int at = static_cast<int>(max(slot, int64_t(0)) % kKv4BlockSlots);
+  uint32_t meta[2][2];
 #pragma unroll
-    for (int v = 0; v < kTokens; ++v) {   // part p is held by lanes 8 p ..
-      const uint32_t y = __shfl_sync(0xffffffffu, meta[v], 8 * p);
-      if (v == u) m = y;
+  for (int plane = 0; plane < 2; ++plane) {
+    uint2 code[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint4 y = x[plane][2 * g], z = x[plane][2 * g + 1];
+      const uint32_t w[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+      code[g] = quantise(w, &meta[plane][g]);
     }
-    const int64_t slot = __shfl_sync(0xffffffffu, mine.slot, u);
-    const int64_t bh = static_cast<int64_t>(__shfl_sync(0xffffffffu, mine.b, u)) * a.H + h;
-    if (slot >= 0) {
-      const int64_t m_off = kv4_block_offset(bh, a.cap, slot) + kKv4MetaOffset +
-                            static_cast<int>(slot % kKv4BlockSlots) * 16 + p * 4;
-      if (in_bounds(m_off, 4, a.blocks_bytes, a.err)) *reinterpret_cast<uint32_t*>(a.cache + m_off) = m;
+    // chunks q and q + 4 of the row: the words of both groups
+    const int64_t off = blk + plane * kKv4VOffset + at * 64 + q * 8;
+    if (slot >= 0 && in_bounds(off, 40, a.blocks_bytes, a.err)) {
+      *reinterpret_cast<uint2*>(a.cache + off) = make_uint2(code[0].x, code[1].x);
+      *reinterpret_cast<uint2*>(a.cache + off + 32) = make_uint2(code[0].y, code[1].y);
     }
   }
-  if (mine.slot >= 0) {
-    const int64_t at = (static_cast<int64_t>(mine.b) * a.H + h) * a.cap + mine.slot;
-    a.weight[at] = 0.f;
-    a.pos[at] = static_cast<int32_t>(a.r.pos0 ? a.r.pos0[mine.b] + (mine.slot - a.r.start[mine.b]) : mine.slot);
+  if (slot < 0) return;
+  const int64_t m_off = blk + kKv4MetaOffset + at * 16;
+  if (q == 0 && in_bounds(m_off, 16, a.blocks_bytes, a.err))
+    *reinterpret_cast<uint4*>(a.cache + m_off) = make_uint4(meta[0][0], meta[0][1], meta[1][0], meta[1][1]);
+  if (q == 1) a.weight[bh * a.cap + slot] = 0.f;
+  if (q == 2)
+    a.pos[bh * a.cap + slot] = static_cast<int32_t>(a.r.pos0 ? a.r.pos0[b] + (slot - a.r.start[b]) : slot);
+}
+
+// bf16(m + s n) of the 8 codes of a word: a nibble under the exponent of 2^7 is
+// that number plus 128; the fused multiply-add rounds once.
+__device__ __forceinline__ uint4 dequantise(uint32_t code, uint32_t meta) {
+  const uint32_t s2 = __byte_perm(meta, 0, 0x1010u), m2 = __byte_perm(meta, 0, 0x3232u), up = code >> 4;
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    // byte e of the codes and of the codes shifted down by a nibble: dims 2 e and 2 e + 1
+    uint32_t n = (__byte_perm(code, up, 0x0400u + e * 0x0101u) & 0x000F000Fu) | 0x43004300u;
+    asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(n) : "r"(0x43004300u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o[e]) : "r"(s2), "r"(n), "r"(m2));
   }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Load: the same split; a lane turns one 32-bit word of codes into 8 bf16.
+template <int T>
 __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const Kv4RowsLaunch a) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t groups = (a.r.rows + kTokens - 1) / kTokens;
+  const int64_t groups = (a.r.rows + T - 1) / T;
   pdl_wait();
   if (item >= groups * a.H) return;
-  const int64_t i0 = item / a.H * kTokens;
+  const int64_t i0 = item / a.H * T;
   const int h = static_cast<int>(item - item / a.H * a.H);
-  const RowPlace mine = place_rows(a.r, i0, a.B, a.cap, a.err);
   const int plane = lane >> 4, l16 = lane & 15;
+  const int c_at = plane * kKv4VOffset + (l16 & 7) * 8 + (l16 >> 3) * 4, m_at = plane * 8 + (l16 >> 3) * 4;
   uint16_t* dst = static_cast<uint16_t*>(plane ? a.r.v : a.r.k) + row_offset(a.r, i0, h) + l16 * 8;
-  uint32_t code[kTokens], meta[kTokens];
-  uint32_t there = 0;
+  const RowPlace mine = place_rows<T>(a.r, i0, a.B, a.cap, a.err);
+  if (one_run<T>(mine)) {
+    const int64_t slot0 = __shfl_sync(0xffffffffu, mine.slot, 0);
+    const int64_t blk = kv4_block_offset(static_cast<int64_t>(__shfl_sync(0xffffffffu, mine.b, 0)) * a.H + h, a.cap,
+                                         slot0);
+    const int at = static_cast<int>(slot0 % kKv4BlockSlots);
+    uint32_t code[T], meta[T];
 #pragma unroll
-  for (int u = 0; u < kTokens; ++u) {
-    const int64_t slot = __shfl_sync(0xffffffffu, mine.slot, u);
-    const int b = __shfl_sync(0xffffffffu, mine.b, u);
-    code[u] = meta[u] = 0;
-    if (slot >= 0) {
-      there |= 1u << u;
-      const int64_t blk = kv4_block_offset(static_cast<int64_t>(b) * a.H + h, a.cap, slot);
-      const int at = static_cast<int>(slot % kKv4BlockSlots);
-      const int64_t c_off = blk + plane * kKv4VOffset + at * 64 + (l16 & 7) * 8 + (l16 >> 3) * 4;
-      const int64_t m_off = blk + kKv4MetaOffset + at * 16 + plane * 8 + (l16 >> 3) * 4;
-      if (in_bounds(c_off, 4, a.blocks_bytes, a.err)) code[u] = *reinterpret_cast<const uint32_t*>(a.cache + c_off);
+    for (int u = 0; u < T; ++u) {
+      const int64_t off = blk + (code_row(at + u) + c_at), m_off = blk + (meta_row(at + u) + m_at);
+      code[u] = meta[u] = 0;
+      if (in_bounds(off, 4, a.blocks_bytes, a.err)) code[u] = *reinterpret_cast<const uint32_t*>(a.cache + off);
       if (in_bounds(m_off, 4, a.blocks_bytes, a.err)) meta[u] = *reinterpret_cast<const uint32_t*>(a.cache + m_off);
     }
-  }
 #pragma unroll
-  for (int u = 0; u < kTokens; ++u) {
-    const float s = bf16_lo(meta[u]), m = bf16_hi(meta[u]);
-    const uint32_t even = code[u] & 0x0F0F0F0Fu, odd = (code[u] >> 4) & 0x0F0F0F0Fu;
-    uint32_t o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // a byte under the exponent of 2^23 is that number plus 2^23; s n is
-      // exact in fp32 (8 + 4 bits): one rounding at the sum, one to bf16
-      const float n0 = __uint_as_float(__byte_perm(even, 0x4B000000u, 0x7440u + e)) - 8388608.f;
-      const float n1 = __uint_as_float(__byte_perm(odd, 0x4B000000u, 0x7440u + e)) - 8388608.f;
-      const float lo = fmaf(s, n0, m), hi = fmaf(s, n1, m);
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[e]) : "f"(hi), "f"(lo));
+    for (int u = 0; u < T; ++u)
+      *reinterpret_cast<uint4*>(dst + u * a.r.token_stride) = dequantise(code[u], meta[u]);
+  } else if (T > 1) {
+#pragma unroll 1
+    for (int u = 0; u < T; ++u) {
+      const int64_t slot = __shfl_sync(0xffffffffu, mine.slot, u);
+      const int b = __shfl_sync(0xffffffffu, mine.b, u);
+      if (slot < 0) continue;
+      const int64_t blk = kv4_block_offset(static_cast<int64_t>(b) * a.H + h, a.cap, slot);
+      const int at = static_cast<int>(slot % kKv4BlockSlots);
+      const int64_t off = blk + (code_row(at) + c_at), m_off = blk + (meta_row(at) + m_at);
+      if (in_bounds(off, 4, a.blocks_bytes, a.err) && in_bounds(m_off, 4, a.blocks_bytes, a.err))
+        *reinterpret_cast<uint4*>(dst + u * a.r.token_stride) =
+            dequantise(*reinterpret_cast<const uint32_t*>(a.cache + off),
+                       *reinterpret_cast<const uint32_t*>(a.cache + m_off));
     }
-    if (there >> u & 1)
-      *reinterpret_cast<uint4*>(dst + u * a.r.token_stride) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
 // ---------------------------------------------------------------- eviction
 
 constexpr int kSelThreads = 1024;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
 
 // Larger key = larger weight; equal weights (also -0 and +0) have equal keys;
 // NaN ranks below everything.
@@ -319,13 +380,17 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
 // the destination's position array (the gather replaces them by positions).
 //
 // A cluster of blocks shares a pair, each block a run of its slots.  The k-th
-// largest key is found by its digits (11, 11 and 10 bits): every block makes a
+// largest key is found digit by digit (four of 8 bits): every block makes a
 // histogram of the digit over its keys that agree so far, and all add up the
-// cluster's histograms through distributed shared memory.  Their own
-// histograms then say how many slots each block keeps, so the kept slots are
-// numbered without another pass.
+// cluster's histograms through distributed shared memory.  A histogram has a
+// column for every lane, so that lanes never meet in a counter: weights share
+// few exponents, and many are equal (one counter a bin took 112 us for 56 pairs
+// of 104,448 slots, nearly all of it in the first digit's collisions).  Their
+// own histograms then say how many slots each block keeps, so the kept slots
+// are numbered without another pass.
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictLaunch a, int cluster) {
-  __shared__ __align__(8) uint32_t hist[3][kBins];
+  __shared__ __align__(16) uint32_t hist[kBins][32];
+  __shared__ uint32_t sums[4][kBins];
   __shared__ uint32_t warp_sums[32];
   __shared__ uint32_t s_bin, s_above;
   __shared__ uint32_t s_sure, s_equal;   // slots of this block's run: kept for sure, equal to the k-th
@@ -333,7 +398,9 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
   const int rank = static_cast<int>(blockIdx.x) % cluster;
   const int64_t bh = blockIdx.x / cluster;
   const int b = static_cast<int>(bh / a.H);
-  for (int i = threadIdx.x; i < 3 * kBins; i += blockDim.x) (&hist[0][0])[i] = 0;
+  uint4* const cells = reinterpret_cast<uint4*>(&hist[0][0]) + 2 * threadIdx.x;   // 8 counters of bin threadIdx.x / 4
+  static_assert(kBins * 32 == kSelThreads * 8, "a thread has 8 counters");
+  cells[0] = cells[1] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) s_sure = s_equal = 0;
   __syncthreads();
   pdl_wait();
@@ -354,9 +421,8 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
   if (k > 0) {
     uint32_t mask = 0, above = 0;
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const uint32_t digit = pass == 2 ? 1023u : 2047u;
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
       for (int i = i_begin + 4 * threadIdx.x; i < i_end; i += 4 * blockDim.x) {
         // (capacities are multiples of 4: the load stays inside the pair)
         const float4 v = *reinterpret_cast<const float4*>(w + i);
@@ -365,33 +431,34 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
         for (int e = 0; e < 4; ++e) {
           const uint32_t key = weight_key(x[e]);
           if (i + e < i_end && i + e >= c0 && i + e < c1 && (key & mask) == prefix)
-            atomicAdd(&hist[pass][(key >> shift) & digit], 1u);
+            atomicAdd(&hist[(key >> shift) & 255u][threadIdx.x & 31], 1u);
         }
       }
+      __syncthreads();
+      const uint4 y0 = cells[0], y1 = cells[1];
+      cells[0] = cells[1] = make_uint4(0, 0, 0, 0);
+      uint32_t own = y0.x + y0.y + y0.z + y0.w + y1.x + y1.y + y1.z + y1.w;
+      own += __shfl_xor_sync(0xffffffffu, own, 1);
+      own += __shfl_xor_sync(0xffffffffu, own, 2);
+      if ((threadIdx.x & 3) == 0) sums[pass][threadIdx.x >> 2] = own;
       __syncwarp();
       cluster_sync();
-      // bins from the top: thread t holds bins kBins-1-2t and kBins-2-2t
-      const uint32_t top = kBins - 2 - 2 * threadIdx.x;
-      uint32_t h0 = 0, h1 = 0;
-      for (int r = 0; r < cluster; ++r) {
-        h1 += ld_cluster(&hist[pass][top], r);
-        h0 += ld_cluster(&hist[pass][top + 1], r);
-      }
-      uint32_t total;
-      const uint32_t upto = block_scan(h0 + h1, warp_sums, &total);
-      const uint32_t before = upto - h0 - h1;
-      if (before < left && left <= upto) {
-        const bool first = left <= before + h0;
-        s_bin = top + (first ? 1 : 0);
-        s_above = before + (first ? 0 : h0);
+      // bins from the top, one a thread
+      const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
+      uint32_t all = 0, total;
+      if (bin >= 0)
+        for (int r = 0; r < cluster; ++r) all += ld_cluster(&sums[pass][bin], r);
+      const uint32_t upto = block_scan(all, warp_sums, &total), before = upto - all;
+      if (before < left && left <= upto) {   // (bin >= 0: the others have upto == before)
+        s_bin = bin;
+        s_above = before;
       }
       __syncthreads();
-      const uint32_t bin = s_bin;
       left -= s_above;
-      prefix |= bin << shift;
-      mask |= digit << shift;
-      above += (top > bin ? hist[pass][top] : 0u) + (top + 1 > bin ? hist[pass][top + 1] : 0u);   // this block's own
-      if (pass == 2 && threadIdx.x == 0) s_equal = hist[pass][bin];
+      prefix |= s_bin << shift;
+      mask |= 255u << shift;
+      if (bin > static_cast<int>(s_bin)) above += sums[pass][bin];   // this block's own
+      if (pass == 3 && threadIdx.x == 0) s_equal = sums[pass][s_bin];
       __syncthreads();
     }
     if (above) atomicAdd(&s_sure, above);
@@ -496,12 +563,15 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4EvictLaun
 }  // namespace
 
 cudaError_t launch_kv4_rows(bool load, const Kv4RowsLaunch& a, cudaStream_t stream) {
-  const int64_t items = (a.r.rows + kTokens - 1) / kTokens * a.H;
-  if (items == 0) return cudaSuccess;
+  if (a.r.rows == 0) return cudaSuccess;
+  // The load takes runs of tokens where sequences bring enough of them, and a
+  // warp a token where they bring one or a few, which a run would take one by one.
+  const bool runs = !load || a.r.rows >= static_cast<int64_t>(4 * kRun) * a.B;
+  const int64_t items = runs ? (a.r.rows + kRun - 1) / kRun * a.H : a.r.rows * a.H;
   const int64_t grid = (items + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_after(load ? kv4_load_kernel : kv4_append_kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, 1,
-                      stream, a);
+  const auto kernel = !load ? kv4_append_kernel : (runs ? kv4_load_kernel<kRun> : kv4_load_kernel<1>);
+  return launch_after(kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_kv4_evict(const Kv4EvictLaunch& a, cudaStream_t stream) {
