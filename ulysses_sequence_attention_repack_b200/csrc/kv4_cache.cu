@@ -334,6 +334,8 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const Kv4RowsLaunch 
 
 constexpr int kSelThreads = 1024;
 constexpr int kBins = 256;
+constexpr int kMaxCluster = 8;
+constexpr int kHeldKeys = 40960;   // 160 KB beside the counters' 37
 
 // Larger key = larger weight; equal weights (also -0 and +0) have equal keys;
 // NaN ranks below everything.
@@ -343,31 +345,15 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Block-wide inclusive scan of v (every thread calls it); *total gets the sum.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, uint32_t* total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  uint32_t x = v;
+// Inclusive scan over the lanes of a warp.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
   }
-  if (lane == 31) warp_sums[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    uint32_t s = lane < static_cast<int>(blockDim.x >> 5) ? warp_sums[lane] : 0u;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s += y;
-    }
-    warp_sums[lane] = s;
-  }
-  __syncthreads();
-  const uint32_t before = w ? warp_sums[w - 1] : 0u;
-  *total = warp_sums[(blockDim.x >> 5) - 1];
-  __syncthreads();
-  return before + x;
+  return x;
 }
 
 __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
@@ -377,32 +363,37 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
 }
 
 // The slots that one (sequence, head) pair keeps, in their order, written into
-// the destination's position array (the gather replaces them by positions).
+// the destination's position array (the gather replaces them by positions):
+// those of the `keep` largest keys, where a protected slot's key is above that
+// of any weight and equal keys count from the lowest slot.
 //
-// A cluster of blocks shares a pair, each block a run of its slots.  The k-th
-// largest key is found digit by digit (four of 8 bits): every block makes a
-// histogram of the digit over its keys that agree so far, and all add up the
-// cluster's histograms through distributed shared memory.  A histogram has a
-// column for every lane, so that lanes never meet in a counter: weights share
-// few exponents, and many are equal (one counter a bin took 112 us for 56 pairs
-// of 104,448 slots, nearly all of it in the first digit's collisions).  Their
-// own histograms then say how many slots each block keeps, so the kept slots
-// are numbered without another pass.
-__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictLaunch a, int cluster) {
+// A cluster of blocks shares a pair, each block a run of its slots whose keys
+// it holds in shared memory (or, past kHeldKeys, makes anew from the weights
+// each time).  The keep-th largest key is found digit by digit (four of 8
+// bits): every block makes a histogram of the digit over its keys that agree
+// so far, and all add up the cluster's histograms through distributed shared
+// memory.  A histogram has a column for every lane, so that lanes never meet in
+// a counter: weights share few exponents, and many are equal (with one counter
+// a bin the first digit's collisions alone took 100 us for 56 pairs of 104,448
+// slots).  Their own histograms then say how many slots each block keeps, so
+// the kept slots are numbered without another exchange.
+__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictLaunch a, int cluster, int held_keys) {
+  constexpr int kSelWarps = kSelThreads / 32;
+  extern __shared__ __align__(16) uint32_t held[];
   __shared__ __align__(16) uint32_t hist[kBins][32];
   __shared__ uint32_t sums[4][kBins];
-  __shared__ uint32_t warp_sums[32];
+  __shared__ uint32_t scan_sums[kBins / 32], warp_sure[kSelWarps], warp_equal[kSelWarps];
   __shared__ uint32_t s_bin, s_above;
-  __shared__ uint32_t s_sure, s_equal;   // slots of this block's run: kept for sure, equal to the k-th
+  __shared__ uint32_t s_sure, s_equal;   // slots of this block's run: above the keep-th key, equal to it
   pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(blockIdx.x) % cluster;
   const int64_t bh = blockIdx.x / cluster;
   const int b = static_cast<int>(bh / a.H);
   uint4* const cells = reinterpret_cast<uint4*>(&hist[0][0]) + 2 * threadIdx.x;   // 8 counters of bin threadIdx.x / 4
   static_assert(kBins * 32 == kSelThreads * 8, "a thread has 8 counters");
   cells[0] = cells[1] = make_uint4(0, 0, 0, 0);
-  if (threadIdx.x == 0) s_sure = s_equal = 0;
-  __syncthreads();
+  if (threadIdx.x == 0) s_sure = 0;
   pdl_wait();
   const int n = kv4_length(a.lengths[b], a.src_cap, threadIdx.x == 0 ? a.err : nullptr);
   const int kept = n < a.keep ? n : a.keep;
@@ -415,98 +406,127 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
     return;
   }
   const float* w = a.src_weight + bh * a.src_cap;
-  const int c0 = a.sink, c1 = n - a.recent;   // candidates [c0, c1): more than k of them, since n > keep
-  const uint32_t k = static_cast<uint32_t>(a.keep - a.sink - a.recent);
-  uint32_t prefix = 0, left = k;              // the k-th largest key's digits so far; its rank among those that agree
-  if (k > 0) {
-    uint32_t mask = 0, above = 0;
+  const int c0 = a.sink, c1 = n - a.recent;   // slots outside [c0, c1) are protected
+  const auto make_keys = [&](int i) {   // of slots i .. i + 3 (capacities are multiples of 4: the load stays inside the pair)
+    const float4 v = *reinterpret_cast<const float4*>(w + i);
+    uint32_t k[4] = {weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w)};
+    if (i < c0 || i + 3 >= c1) {
 #pragma unroll
-    for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass;
-      for (int i = i_begin + 4 * threadIdx.x; i < i_end; i += 4 * blockDim.x) {
-        // (capacities are multiples of 4: the load stays inside the pair)
-        const float4 v = *reinterpret_cast<const float4*>(w + i);
-        const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t key = weight_key(x[e]);
-          if (i + e < i_end && i + e >= c0 && i + e < c1 && (key & mask) == prefix)
-            atomicAdd(&hist[(key >> shift) & 255u][threadIdx.x & 31], 1u);
-        }
-      }
-      __syncthreads();
-      const uint4 y0 = cells[0], y1 = cells[1];
-      cells[0] = cells[1] = make_uint4(0, 0, 0, 0);
-      uint32_t own = y0.x + y0.y + y0.z + y0.w + y1.x + y1.y + y1.z + y1.w;
-      own += __shfl_xor_sync(0xffffffffu, own, 1);
-      own += __shfl_xor_sync(0xffffffffu, own, 2);
-      if ((threadIdx.x & 3) == 0) sums[pass][threadIdx.x >> 2] = own;
-      __syncwarp();
-      cluster_sync();
-      // bins from the top, one a thread
-      const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
-      uint32_t all = 0, total;
-      if (bin >= 0)
-        for (int r = 0; r < cluster; ++r) all += ld_cluster(&sums[pass][bin], r);
-      const uint32_t upto = block_scan(all, warp_sums, &total), before = upto - all;
-      if (before < left && left <= upto) {   // (bin >= 0: the others have upto == before)
-        s_bin = bin;
-        s_above = before;
-      }
-      __syncthreads();
-      left -= s_above;
-      prefix |= s_bin << shift;
-      mask |= 255u << shift;
-      if (bin > static_cast<int>(s_bin)) above += sums[pass][bin];   // this block's own
-      if (pass == 3 && threadIdx.x == 0) s_equal = sums[pass][s_bin];
-      __syncthreads();
+      for (int e = 0; e < 4; ++e)
+        if (i + e < c0 || i + e >= c1) k[e] = 0xffffffffu;
     }
-    if (above) atomicAdd(&s_sure, above);
-  }
+    return make_uint4(k[0], k[1], k[2], k[3]);
+  };
+  const bool hold = run <= held_keys;
+  if (hold)
+#pragma unroll 4
+    for (int i = i_begin + 4 * threadIdx.x; i < i_end; i += 4 * kSelThreads)
+      *reinterpret_cast<uint4*>(held + (i - i_begin)) = make_keys(i);
+  const auto keys = [&](int i) { return hold ? *reinterpret_cast<const uint4*>(held + (i - i_begin)) : make_keys(i); };
   __syncthreads();
-  if (threadIdx.x == 0)   // the protected slots of this run
-    s_sure += static_cast<uint32_t>(max(0, min(i_end, c0) - i_begin) + max(0, i_end - max(i_begin, c1)));
-  __syncwarp();
-  cluster_sync();
-  uint32_t base_keep = 0, base_equal = 0;
-  for (int r = 0; r < rank; ++r) {
-    base_keep += ld_cluster(&s_sure, r);
-    base_equal += ld_cluster(&s_equal, r);
-  }
-  // Keep the protected slots, the keys above the k-th and the first `left` of
-  // its equals, numbered by a running scan; the two counts are scanned
-  // together, 16 bits each (a chunk has 4096 slots).
-  for (int i0 = i_begin; i0 < i_end; i0 += 4 * blockDim.x) {
-    const int i = i0 + 4 * threadIdx.x;
-    uint32_t sure = 0, equal = 0;   // bit e: slot i + e
-    if (i < i_end) {
-      const float4 v = *reinterpret_cast<const float4*>(w + i);
-      const float x[4] = {v.x, v.y, v.z, v.w};
+
+  uint32_t prefix = 0, mask = 0, left = a.keep;   // the key's digits so far; its rank among the keys that agree
+  uint32_t above = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (i + e >= i_end) continue;
-        if (i + e < c0 || i + e >= c1) {
-          sure |= 1u << e;
-        } else if (k > 0) {
-          const uint32_t key = weight_key(x[e]);
-          if (key > prefix) sure |= 1u << e;
-          if (key == prefix) equal |= 1u << e;
-        }
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int i = i_begin + 4 * threadIdx.x; i < i_end; i += 4 * kSelThreads) {
+      const uint4 v = keys(i);
+      const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((k[e] & mask) == prefix && i + e < i_end) atomicAdd(&hist[(k[e] >> shift) & 255u][lane], 1u);
+    }
+    __syncthreads();
+    const uint4 y0 = cells[0], y1 = cells[1];
+    cells[0] = cells[1] = make_uint4(0, 0, 0, 0);
+    uint32_t own = y0.x + y0.y + y0.z + y0.w + y1.x + y1.y + y1.z + y1.w;
+    own += __shfl_xor_sync(0xffffffffu, own, 1);
+    own += __shfl_xor_sync(0xffffffffu, own, 2);
+    if ((threadIdx.x & 3) == 0) sums[pass][threadIdx.x >> 2] = own;
+    __syncwarp();
+    cluster_sync();
+    // the first 8 warps: bins from the top, one a thread
+    const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
+    uint32_t all = 0, upto = 0;
+    if (warp < kBins / 32) {
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < cluster) all += ld_cluster(&sums[pass][bin], r);
+      upto = warp_scan(all);
+      if (lane == 31) scan_sums[warp] = upto;
+    }
+    __syncthreads();
+    if (warp < kBins / 32) {
+      for (int v = 0; v < warp; ++v) upto += scan_sums[v];
+      if (upto - all < left && left <= upto) {
+        s_bin = bin;
+        s_above = upto - all;
       }
     }
-    const uint32_t mine = __popc(sure) | (__popc(equal) << 16);
-    uint32_t total;
-    const uint32_t upto = block_scan(mine, warp_sums, &total) - mine;
-    uint32_t keep_before = base_keep + (upto & 0xFFFFu), equal_before = base_equal + (upto >> 16);
+    __syncthreads();
+    left -= s_above;
+    prefix |= s_bin << shift;
+    mask |= 255u << shift;
+    if (bin > static_cast<int>(s_bin)) above += sums[pass][bin];   // this block's own
+  }
+  if (above) atomicAdd(&s_sure, above);
+  if (threadIdx.x == 0) s_equal = sums[3][prefix & 255u];
+
+  // each warp's part of the run: how many of its slots are above the key, and equal to it
+  const int part = (run / 4 + kSelWarps - 1) / kSelWarps * 4;
+  const int p_begin = min(i_end, i_begin + warp * part), p_end = min(i_end, p_begin + part);
+  uint32_t sure = 0, equal = 0;
+  for (int i = p_begin + 4 * lane; i < p_end; i += 128) {
+    const uint4 v = keys(i);
+    const uint32_t k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const bool is_sure = sure >> e & 1, is_equal = equal >> e & 1;
-      if (is_sure || (is_equal && equal_before < left)) idx[keep_before + min(equal_before, left)] = i + e;
-      keep_before += is_sure;
-      equal_before += is_equal;
+      sure += k[e] > prefix && i + e < p_end;
+      equal += k[e] == prefix && i + e < p_end;
     }
-    base_keep += total & 0xFFFFu;
-    base_equal += total >> 16;
+  }
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) {
+    warp_sure[warp] = sure;
+    warp_equal[warp] = equal;
+  }
+  __syncthreads();
+  cluster_sync();   // (also s_sure and s_equal)
+  uint32_t keep_before = 0, equal_before = 0;
+  // lane r: block r's counts, and warp r's of this block
+  keep_before = (lane < rank ? ld_cluster(&s_sure, lane) : 0u) + (lane < warp ? warp_sure[lane] : 0u);
+  equal_before = (lane < rank ? ld_cluster(&s_equal, lane) : 0u) + (lane < warp ? warp_equal[lane] : 0u);
+  keep_before = __reduce_add_sync(0xffffffffu, keep_before);
+  equal_before = __reduce_add_sync(0xffffffffu, equal_before);
+  for (int i0 = p_begin; i0 < p_end; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    uint32_t is_sure = 0, is_equal = 0;   // bit e: slot i + e
+    if (i < p_end) {
+      const uint4 v = keys(i);
+      const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (i + e >= p_end) continue;
+        is_sure |= (k[e] > prefix ? 1u : 0u) << e;
+        is_equal |= (k[e] == prefix ? 1u : 0u) << e;
+      }
+    }
+    if (!__any_sync(0xffffffffu, is_sure | is_equal)) continue;
+    const uint32_t mine = __popc(is_sure) | (__popc(is_equal) << 16);
+    const uint32_t upto = warp_scan(mine);
+    uint32_t s = keep_before + ((upto - mine) & 0xFFFFu), q = equal_before + ((upto - mine) >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t is_s = is_sure >> e & 1u, is_q = is_equal >> e & 1u;
+      if (is_s || (is_q && q < left)) idx[s + min(q, left)] = i + e;
+      s += is_s;
+      q += is_q;
+    }
+    const uint32_t total = __shfl_sync(0xffffffffu, upto, 31);
+    keep_before += total & 0xFFFFu;
+    equal_before += total >> 16;
   }
   __syncwarp();
   cluster_sync();   // no block ends while another may read its shared memory
@@ -577,10 +597,20 @@ cudaError_t launch_kv4_rows(bool load, const Kv4RowsLaunch& a, cudaStream_t stre
 cudaError_t launch_kv4_evict(const Kv4EvictLaunch& a, cudaStream_t stream) {
   const int pairs = a.B * a.H;
   // blocks that share a pair: about 8,192 slots of the longest each
-  int cluster = 1;
-  while (cluster < 8 && a.src_cap > 8192ll * cluster) cluster *= 2;
-  cudaError_t e = launch_after(kv4_select_kernel, dim3(static_cast<unsigned>(pairs) * cluster), kSelThreads, 0, cluster,
-                               stream, a, cluster);
+  int cluster = 1, dev = 0;
+  while (cluster < kMaxCluster && a.src_cap > 8192ll * cluster) cluster *= 2;
+  // keys of a whole run where they fit (16,384 leave room for two blocks an SM)
+  const int64_t run = (a.src_cap + 4 * cluster - 1) / (4 * cluster) * 4;
+  const int held = static_cast<int>(run <= kHeldKeys ? run : 0);
+  static PerDeviceOnce once;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = once.run(dev, [] {
+      return cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
+    });
+  if (e != cudaSuccess) return e;
+  e = launch_after(kv4_select_kernel, dim3(static_cast<unsigned>(pairs) * cluster), kSelThreads, held * 4, cluster,
+                   stream, a, cluster, held);
   if (e != cudaSuccess) return e;
   const int64_t most = a.keep < a.src_cap ? a.keep : a.src_cap;
   return launch_after(kv4_gather_kernel,
