@@ -499,24 +499,16 @@ class KV4Plan:
     def __init__(self, handle: int, batch: int, heads: int, D: int, capacity: int):
         self._h = ctypes.c_void_p(handle)
         self.batch, self.heads, self.D, self.capacity = batch, heads, D, capacity
+        lib = load()
+        self.cache_bytes: int = lib.ulysses_kv4_cache_bytes(self._h)
+        self.weight_offset: int = lib.ulysses_kv4_weight_offset(self._h)
+        self.position_offset: int = lib.ulysses_kv4_position_offset(self._h)
 
     @property
     def handle(self) -> ctypes.c_void_p:
         if not self._h:
             raise ValueError("plan destroyed")
         return self._h
-
-    @property
-    def cache_bytes(self) -> int:
-        return load().ulysses_kv4_cache_bytes(self.handle)
-
-    @property
-    def weight_offset(self) -> int:
-        return load().ulysses_kv4_weight_offset(self.handle)
-
-    @property
-    def position_offset(self) -> int:
-        return load().ulysses_kv4_position_offset(self.handle)
 
     def workspace_bytes(self, q_heads: int, q_len: int, weights: bool = False) -> int:
         """Workspace of ulysses_kv4_attn."""
@@ -544,33 +536,67 @@ def ulysses_kv4_plan(batch: int, heads: int, D: int, capacity: int) -> KV4Plan:
     return KV4Plan(h.value, int(batch), int(heads), int(D), int(capacity))
 
 
-def _kv4_tensor(where: str, name: str, t, dtype: str, numel: int | None = None):
-    """A CUDA tensor of this type (and, where given, a contiguous one of at least numel elements)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != getattr(torch, dtype):
+# A decoding step makes these calls once a layer, so what they check of their
+# tensors is kept to a few microseconds.
+_types: dict = {}
+
+
+def _kv4_types() -> dict:
+    if not _types:
+        import torch
+        _types.update(tensor=torch.Tensor, uint8=torch.uint8, bf16=torch.bfloat16, int32=torch.int32,
+                      fp32=torch.float32, device=torch.cuda.current_device,
+                      raw_stream=getattr(torch._C, "_cuda_getCurrentRawStream", None))
+    return _types
+
+
+def _kv4_stream(stream, t: dict):
+    if stream is None and t["raw_stream"] is not None:
+        return t["raw_stream"](t["device"]())
+    return _stream(stream)
+
+
+def _kv4_flat(where: str, name: str, x, tensor, dtype, numel: int, dev: int):
+    """The address of a contiguous CUDA tensor on device dev of this type with at least numel elements."""
+    if not isinstance(x, tensor) or not x.is_cuda or x.dtype is not dtype:
         raise TypeError(f"{where}: {name} must be a CUDA tensor of type {dtype}")
-    if numel is not None and (not t.is_contiguous() or t.numel() < numel):
+    if x.numel() < numel or not x.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous with at least {numel} elements")
-    return t
+    if x.get_device() != dev:
+        raise ValueError(f"{where}: {name} is not on the current device")
+    return x.data_ptr()
 
 
-def _kv4_rows(where: str, kv: KV4Plan, cache, k, v, cu, start):
-    """The rows argument of append and load: K and V of one shape and layout,
-    [rows, heads, D] or, split over ranks, [P, rows, heads / P, D]."""
-    _kv4_tensor(where, "cache", cache, "uint8", kv.cache_bytes)
-    _kv4_tensor(where, "k", k, "bfloat16")
-    _kv4_tensor(where, "v", v, "bfloat16")
-    _kv4_tensor(where, "cu", cu, "int32", kv.batch + 1)
-    _kv4_tensor(where, "start", start, "int32", kv.batch)
-    if k.shape != v.shape or k.stride() != v.stride():
+def _kv4_cache(where: str, name: str, kv: KV4Plan, x, t: dict):
+    """The address of a cache of this plan, and the current device, which has to be its own."""
+    if not isinstance(x, t["tensor"]) or not x.is_cuda:
+        raise TypeError(f"{where}: {name} must be a CUDA tensor of type {t['uint8']}")
+    dev = t["device"]()
+    return _kv4_flat(where, name, x, t["tensor"], t["uint8"], kv.cache_bytes, dev), dev
+
+
+def _kv4_rows(where: str, kv: KV4Plan, cache, k, v, cu, start, t: dict):
+    """The common arguments of append and load: K and V of one shape and
+    layout, [rows, heads, D] or, split over ranks, [P, rows, heads / P, D]."""
+    T, i32, bf16 = t["tensor"], t["int32"], t["bf16"]
+    c, dev = _kv4_cache(where, "cache", kv, cache, t)
+    for name, x in (("k", k), ("v", v)):
+        if not isinstance(x, T) or not x.is_cuda or x.dtype is not bf16:
+            raise TypeError(f"{where}: {name} must be a CUDA tensor of type {bf16}")
+        if x.get_device() != dev:
+            raise ValueError(f"{where}: {name} is not on the current device")
+    shape, stride = k.shape, k.stride()
+    if shape != v.shape or stride != v.stride():
         raise ValueError(f"{where}: k and v must have one shape and layout")
-    if k.dim() not in (3, 4) or k.shape[-1] != kv.D or (k.numel() and k.stride(-1) != 1):
+    n = len(shape)
+    if n not in (3, 4) or shape[-1] != kv.D or stride[-1] != 1:
         raise ValueError(f"{where}: k and v are [rows, heads, {kv.D}] or [ranks, rows, heads / ranks, {kv.D}]")
-    ranks, (rows, hl) = (k.shape[0] if k.dim() == 4 else 1), k.shape[-3:-1]
-    if ranks * hl != kv.heads:
-        raise ValueError(f"{where}: {ranks * hl} heads, the plan has {kv.heads}")
-    rank_stride = k.stride(0) if k.dim() == 4 else 0
-    return rows, k.stride(-3), k.stride(-2), rank_stride, hl
+    ranks, rank_stride = (shape[0], stride[0]) if n == 4 else (1, 0)
+    if ranks * shape[-2] != kv.heads:
+        raise ValueError(f"{where}: {ranks * shape[-2]} heads, the plan has {kv.heads}")
+    return (kv.handle, c, k.data_ptr(), v.data_ptr(), shape[-3], stride[-3], stride[-2], rank_stride, shape[-2],
+            _kv4_flat(where, "cu", cu, T, i32, kv.batch + 1, dev),
+            _kv4_flat(where, "start", start, T, i32, kv.batch, dev))
 
 
 def ulysses_kv4_append(kv: KV4Plan, cache, k, v, cu, start, pos0=None, stream=None) -> None:
@@ -579,53 +605,56 @@ def ulysses_kv4_append(kv: KV4Plan, cache, k, v, cu, start, pos0=None, stream=No
     packed rows will do) or [P, rows, heads / P, D] (planes of a head slab).
     pos0: int32 [batch], the position of each sequence's first new row
     (default: its slot)."""
-    rows, ts, hs, rs, hl = _kv4_rows("ulysses_kv4_append", kv, cache, k, v, cu, start)
+    t = _kv4_types()
+    args = _kv4_rows("ulysses_kv4_append", kv, cache, k, v, cu, start, t)
+    p = None
     if pos0 is not None:
-        _kv4_tensor("ulysses_kv4_append", "pos0", pos0, "int32", kv.batch)
-    if rows == 0:
-        return
-    _check(load().ulysses_kv4_append(kv.handle, _ptr(cache), _ptr(k), _ptr(v), rows, ts, hs, rs, hl, _ptr(cu),
-                                     _ptr(start), _ptr(pos0), _stream(stream)), "ulysses_kv4_append")
+        p = _kv4_flat("ulysses_kv4_append", "pos0", pos0, t["tensor"], t["int32"], kv.batch, t["device"]())
+    if args[4]:
+        _check(load().ulysses_kv4_append(*args, p, _kv4_stream(stream, t)), "ulysses_kv4_append")
 
 
 def ulysses_kv4_load(kv: KV4Plan, cache, k, v, cu, start, stream=None) -> None:
     """Bring slots start[b] on back as bf16 rows cu[b] .. cu[b+1]-1 of k and v
     (layouts as ulysses_kv4_append)."""
-    rows, ts, hs, rs, hl = _kv4_rows("ulysses_kv4_load", kv, cache, k, v, cu, start)
-    if rows == 0:
-        return
-    _check(load().ulysses_kv4_load(kv.handle, _ptr(cache), _ptr(k), _ptr(v), rows, ts, hs, rs, hl, _ptr(cu),
-                                   _ptr(start), _stream(stream)), "ulysses_kv4_load")
+    t = _kv4_types()
+    args = _kv4_rows("ulysses_kv4_load", kv, cache, k, v, cu, start, t)
+    if args[4]:
+        _check(load().ulysses_kv4_load(*args, _kv4_stream(stream, t)), "ulysses_kv4_load")
 
 
 def ulysses_kv4_attn(kv: KV4Plan, cache, q, out, lengths, softmax_scale: float, lse=None, causal: bool = False,
                      weights: bool = False, workspace=None, stream=None) -> None:
     """Attention of q, bf16 [batch, q_len, q_heads, D] (any strides of rows and
     heads), over the cache's slots below lengths [batch] (int32) into out, the
-    same shape, contiguous; lse: optional fp32 [batch, q_heads, q_len]."""
-    where = "ulysses_kv4_attn"
-    _kv4_tensor(where, "cache", cache, "uint8", kv.cache_bytes)
-    _kv4_tensor(where, "q", q, "bfloat16")
-    if q.dim() != 4 or q.shape[0] != kv.batch or q.shape[-1] != kv.D or q.stride(-1) != 1:
+    same shape, contiguous; lse: optional fp32 [batch, q_heads, q_len].
+    weights: add each slot's attention weight to the cache's.  workspace: uint8,
+    at least kv.workspace_bytes(q_heads, q_len, weights)."""
+    where, t = "ulysses_kv4_attn", _kv4_types()
+    T = t["tensor"]
+    c, dev = _kv4_cache(where, "cache", kv, cache, t)
+    if not isinstance(q, T) or not q.is_cuda or q.dtype is not t["bf16"]:
+        raise TypeError(f"{where}: q must be a CUDA tensor of type {t['bf16']}")
+    if q.get_device() != dev:
+        raise ValueError(f"{where}: q is not on the current device")
+    shape, stride = q.shape, q.stride()
+    if len(shape) != 4 or shape[0] != kv.batch or shape[3] != kv.D or stride[3] != 1:
         raise ValueError(f"{where}: q is [{kv.batch}, q_len, q_heads, {kv.D}]")
-    B, q_len, q_heads, D = q.shape
-    if q_len > 1 and B > 1 and q.stride(0) != q_len * q.stride(1):
+    B, q_len, q_heads, D = shape
+    if q_len > 1 and B > 1 and stride[0] != q_len * stride[1]:
         raise ValueError(f"{where}: the rows of q must be evenly spaced over sequences and queries")
-    token_stride = q.stride(1) if q_len > 1 else q.stride(0)
-    _kv4_tensor(where, "out", out, "bfloat16", q.numel())
-    _kv4_tensor(where, "lengths", lengths, "int32", B)
-    if out.shape != q.shape:
+    o = _kv4_flat(where, "out", out, T, t["bf16"], B * q_len * q_heads * D, dev)
+    if out.shape != shape:
         raise ValueError(f"{where}: out has q's shape")
-    if lse is not None:
-        _kv4_tensor(where, "lse", lse, "float32", B * q_heads * q_len)
-    nbytes = 0
+    ls = None if lse is None else _kv4_flat(where, "lse", lse, T, t["fp32"], B * q_heads * q_len, dev)
+    ws, nbytes = None, 0
     if workspace is not None:
-        _kv4_tensor(where, "workspace", workspace, "uint8", 0)
-        nbytes = workspace.numel()
-    flags = (ULYSSES_KV4_CAUSAL if causal else 0) | (ULYSSES_KV4_WEIGHTS if weights else 0)
-    _check(load().ulysses_kv4_attn(kv.handle, _ptr(cache), _ptr(q), q_heads, q_len, token_stride, q.stride(2),
-                                   _ptr(out), _ptr(lse), _ptr(lengths), float(softmax_scale), flags, _ptr(workspace),
-                                   nbytes, _stream(stream)), where)
+        ws, nbytes = _kv4_flat(where, "workspace", workspace, T, t["uint8"], 0, dev), workspace.numel()
+    _check(load().ulysses_kv4_attn(kv.handle, c, q.data_ptr(), q_heads, q_len, stride[1] if q_len > 1 else stride[0],
+                                   stride[2], o, ls, _kv4_flat(where, "lengths", lengths, T, t["int32"], B, dev),
+                                   softmax_scale,
+                                   (ULYSSES_KV4_CAUSAL if causal else 0) | (ULYSSES_KV4_WEIGHTS if weights else 0),
+                                   ws, nbytes, _kv4_stream(stream, t)), where)
 
 
 def ulysses_kv4_evict(src_kv: KV4Plan, src_cache, dst_kv: KV4Plan, dst_cache, lengths, new_lengths, keep: int,
@@ -633,13 +662,14 @@ def ulysses_kv4_evict(src_kv: KV4Plan, src_cache, dst_kv: KV4Plan, dst_cache, le
     """Move the slots worth keeping (the first `sink`, the last `recent` and
     those of largest accumulated weight, `keep` in all) into dst_cache, in
     their order; new_lengths [batch] gets min(lengths, keep)."""
-    where = "ulysses_kv4_evict"
-    _kv4_tensor(where, "src_cache", src_cache, "uint8", src_kv.cache_bytes)
-    _kv4_tensor(where, "dst_cache", dst_cache, "uint8", dst_kv.cache_bytes)
-    _kv4_tensor(where, "lengths", lengths, "int32", src_kv.batch)
-    _kv4_tensor(where, "new_lengths", new_lengths, "int32", src_kv.batch)
-    _check(load().ulysses_kv4_evict(src_kv.handle, _ptr(src_cache), dst_kv.handle, _ptr(dst_cache), _ptr(lengths),
-                                    _ptr(new_lengths), int(keep), int(sink), int(recent), _stream(stream)), where)
+    where, t = "ulysses_kv4_evict", _kv4_types()
+    T, i32 = t["tensor"], t["int32"]
+    src, dev = _kv4_cache(where, "src_cache", src_kv, src_cache, t)
+    dst, _ = _kv4_cache(where, "dst_cache", dst_kv, dst_cache, t)
+    _check(load().ulysses_kv4_evict(src_kv.handle, src, dst_kv.handle, dst,
+                                    _kv4_flat(where, "lengths", lengths, T, i32, src_kv.batch, dev),
+                                    _kv4_flat(where, "new_lengths", new_lengths, T, i32, src_kv.batch, dev),
+                                    keep, sink, recent, _kv4_stream(stream, t)), where)
 
 
 def ulysses_kv4_last_device_error(kv: KV4Plan, stream=None) -> int:

@@ -28,6 +28,7 @@
 // capacity], token positions int32 [batch, heads, capacity].
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -77,6 +78,20 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int64_t s
   c.attrs = at;
   c.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+// The current device and its SMs (asked for once a device: the call is on the
+// way of every launch).
+inline cudaError_t current_device_sms(int* dev, int* sms) {
+  static std::atomic<int> known[64] = {};
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  const bool tracked = *dev >= 0 && *dev < 64;
+  *sms = tracked ? known[*dev].load(std::memory_order_relaxed) : 0;
+  if (*sms > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+  if (e == cudaSuccess && tracked) known[*dev].store(*sms, std::memory_order_relaxed);
+  return e;
 }
 
 // A device-side length, held inside 0 .. capacity (and reported if it was not).

@@ -795,8 +795,7 @@ template <int NT, bool kWeights>
 cudaError_t launch_main(const Args& a, int* ctas, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0, sms = 1;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   const int64_t most = smem_bytes(8 * NT, 8 * NT);
   e = once.run(dev, [&] {

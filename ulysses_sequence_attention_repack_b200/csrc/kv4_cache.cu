@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "bounds.cuh"
@@ -334,8 +335,9 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const Kv4RowsLaunch 
 
 constexpr int kSelThreads = 1024;
 constexpr int kBins = 256;
+constexpr int kColumns = 16;
 constexpr int kMaxCluster = 8;
-constexpr int kHeldKeys = 40960;   // 160 KB beside the counters' 37
+constexpr int kHeldKeys = 22528;   // 88 KB
 
 // Larger key = larger weight; equal weights (also -0 and +0) have equal keys;
 // NaN ranks below everything.
@@ -372,27 +374,27 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
 // each time).  The keep-th largest key is found digit by digit (four of 8
 // bits): every block makes a histogram of the digit over its keys that agree
 // so far, and all add up the cluster's histograms through distributed shared
-// memory.  A histogram has a column for every lane, so that lanes never meet in
-// a counter: weights share few exponents, and many are equal (with one counter
-// a bin the first digit's collisions alone took 100 us for 56 pairs of 104,448
-// slots).  Their own histograms then say how many slots each block keeps, so
+// memory.  A histogram has 16 columns, so that at most two lanes of a warp meet
+// in a counter: weights share few exponents, and many are equal (with one
+// counter a bin the first digit's collisions alone took 100 us for 56 pairs of
+// 104,448 slots; 32 columns take twice as long to clear and add up).  Their own histograms then say how many slots each block keeps, so
 // the kept slots are numbered without another exchange.
-__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictLaunch a, int cluster, int held_keys) {
+template <bool kHeld>
+__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictLaunch a, int cluster) {
   constexpr int kSelWarps = kSelThreads / 32;
   extern __shared__ __align__(16) uint32_t held[];
-  __shared__ __align__(16) uint32_t hist[kBins][32];
+  __shared__ __align__(16) uint32_t hist[kBins][kColumns];
   __shared__ uint32_t sums[4][kBins];
   __shared__ uint32_t scan_sums[kBins / 32], warp_sure[kSelWarps], warp_equal[kSelWarps];
   __shared__ uint32_t s_bin, s_above;
   __shared__ uint32_t s_sure, s_equal;   // slots of this block's run: above the keep-th key, equal to it
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, column = lane & (kColumns - 1);
   const int rank = static_cast<int>(blockIdx.x) % cluster;
   const int64_t bh = blockIdx.x / cluster;
   const int b = static_cast<int>(bh / a.H);
-  uint4* const cells = reinterpret_cast<uint4*>(&hist[0][0]) + 2 * threadIdx.x;   // 8 counters of bin threadIdx.x / 4
-  static_assert(kBins * 32 == kSelThreads * 8, "a thread has 8 counters");
-  cells[0] = cells[1] = make_uint4(0, 0, 0, 0);
+  uint4* const cells = reinterpret_cast<uint4*>(&hist[0][0]) + threadIdx.x;   // 4 counters of bin threadIdx.x / 4
+  static_assert(kBins * kColumns == 4 * kSelThreads, "a thread has 4 counters");
+  *cells = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) s_sure = 0;
   pdl_wait();
   const int n = kv4_length(a.lengths[b], a.src_cap, threadIdx.x == 0 ? a.err : nullptr);
@@ -407,40 +409,67 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
   }
   const float* w = a.src_weight + bh * a.src_cap;
   const int c0 = a.sink, c1 = n - a.recent;   // slots outside [c0, c1) are protected
-  const auto make_keys = [&](int i) {   // of slots i .. i + 3 (capacities are multiples of 4: the load stays inside the pair)
+  // The keys of slots i .. i + 3 (capacities are multiples of 4: the load stays
+  // inside the pair).  Slots behind the length, which follow the very last
+  // one only, get the lowest key: the first of its equals are kept, and there
+  // are enough of them before these.
+  const auto make_keys = [&](int i) {
     const float4 v = *reinterpret_cast<const float4*>(w + i);
     uint32_t k[4] = {weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w)};
     if (i < c0 || i + 3 >= c1) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (i + e < c0 || i + e >= c1) k[e] = 0xffffffffu;
+        if (i + e < c0 || i + e >= c1) k[e] = i + e < n ? 0xffffffffu : 0u;
     }
     return make_uint4(k[0], k[1], k[2], k[3]);
   };
-  const bool hold = run <= held_keys;
-  if (hold)
-#pragma unroll 4
-    for (int i = i_begin + 4 * threadIdx.x; i < i_end; i += 4 * kSelThreads)
-      *reinterpret_cast<uint4*>(held + (i - i_begin)) = make_keys(i);
-  const auto keys = [&](int i) { return hold ? *reinterpret_cast<const uint4*>(held + (i - i_begin)) : make_keys(i); };
+  const auto keys = [&](int i) {
+    if constexpr (kHeld)
+      return *reinterpret_cast<const uint4*>(held + (i - i_begin));
+    else
+      return make_keys(i);
+  };
+  const auto key_of = [&](int i) {
+    if constexpr (kHeld)
+      return held[i - i_begin];
+    else
+      return i < c0 || i >= c1 ? 0xffffffffu : weight_key(w[i]);
+  };
   __syncthreads();
 
-  uint32_t prefix = 0, mask = 0, left = a.keep;   // the key's digits so far; its rank among the keys that agree
+  uint32_t prefix = 0, left = a.keep;   // the key's digits so far; its rank among the keys that agree
   uint32_t above = 0;
 #pragma unroll
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
-    for (int i = i_begin + 4 * threadIdx.x; i < i_end; i += 4 * kSelThreads) {
-      const uint4 v = keys(i);
-      const uint32_t k[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if ((k[e] & mask) == prefix && i + e < i_end) atomicAdd(&hist[(k[e] >> shift) & 255u][lane], 1u);
+    if (pass == 0) {
+#pragma unroll 2
+      for (int i = i_begin + 4 * threadIdx.x; i < i_end; i += 4 * kSelThreads) {
+        const uint4 v = make_keys(i);
+        if constexpr (kHeld) *reinterpret_cast<uint4*>(held + (i - i_begin)) = v;
+        atomicAdd(&hist[v.x >> 24][column], 1u);
+        atomicAdd(&hist[v.y >> 24][column], 1u);
+        atomicAdd(&hist[v.z >> 24][column], 1u);
+        atomicAdd(&hist[v.w >> 24][column], 1u);
+      }
+    } else {
+      const uint32_t want = prefix >> (shift + 8);
+#pragma unroll 2
+      for (int i = i_begin + 4 * threadIdx.x; i < i_end; i += 4 * kSelThreads) {
+        const uint4 v = keys(i);
+        const bool x = v.x >> (shift + 8) == want, y = v.y >> (shift + 8) == want, z = v.z >> (shift + 8) == want,
+                   w4 = v.w >> (shift + 8) == want;
+        if (!(x || y || z || w4)) continue;   // few keys agree with a digit or two
+        if (x) atomicAdd(&hist[(v.x >> shift) & 255u][column], 1u);
+        if (y) atomicAdd(&hist[(v.y >> shift) & 255u][column], 1u);
+        if (z) atomicAdd(&hist[(v.z >> shift) & 255u][column], 1u);
+        if (w4) atomicAdd(&hist[(v.w >> shift) & 255u][column], 1u);
+      }
     }
     __syncthreads();
-    const uint4 y0 = cells[0], y1 = cells[1];
-    cells[0] = cells[1] = make_uint4(0, 0, 0, 0);
-    uint32_t own = y0.x + y0.y + y0.z + y0.w + y1.x + y1.y + y1.z + y1.w;
+    const uint4 y = *cells;
+    *cells = make_uint4(0, 0, 0, 0);
+    uint32_t own = y.x + y.y + y.z + y.w;
     own += __shfl_xor_sync(0xffffffffu, own, 1);
     own += __shfl_xor_sync(0xffffffffu, own, 2);
     if ((threadIdx.x & 3) == 0) sums[pass][threadIdx.x >> 2] = own;
@@ -467,14 +496,13 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
     __syncthreads();
     left -= s_above;
     prefix |= s_bin << shift;
-    mask |= 255u << shift;
     if (bin > static_cast<int>(s_bin)) above += sums[pass][bin];   // this block's own
   }
   if (above) atomicAdd(&s_sure, above);
   if (threadIdx.x == 0) s_equal = sums[3][prefix & 255u];
 
   // each warp's part of the run: how many of its slots are above the key, and equal to it
-  const int part = (run / 4 + kSelWarps - 1) / kSelWarps * 4;
+  const int part = ((run + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int p_begin = min(i_end, i_begin + warp * part), p_end = min(i_end, p_begin + part);
   uint32_t sure = 0, equal = 0;
   for (int i = p_begin + 4 * lane; i < p_end; i += 128) {
@@ -482,8 +510,8 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
     const uint32_t k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      sure += k[e] > prefix && i + e < p_end;
-      equal += k[e] == prefix && i + e < p_end;
+      sure += k[e] > prefix;
+      equal += k[e] == prefix;
     }
   }
   sure = __reduce_add_sync(0xffffffffu, sure);
@@ -500,34 +528,22 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
   equal_before = (lane < rank ? ld_cluster(&s_equal, lane) : 0u) + (lane < warp ? warp_equal[lane] : 0u);
   keep_before = __reduce_add_sync(0xffffffffu, keep_before);
   equal_before = __reduce_add_sync(0xffffffffu, equal_before);
-  for (int i0 = p_begin; i0 < p_end; i0 += 128) {
-    const int i = i0 + 4 * lane;
-    uint32_t is_sure = 0, is_equal = 0;   // bit e: slot i + e
-    if (i < p_end) {
-      const uint4 v = keys(i);
-      const uint32_t k[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (i + e >= p_end) continue;
-        is_sure |= (k[e] > prefix ? 1u : 0u) << e;
-        is_equal |= (k[e] == prefix ? 1u : 0u) << e;
-      }
-    }
-    if (!__any_sync(0xffffffffu, is_sure | is_equal)) continue;
-    const uint32_t mine = __popc(is_sure) | (__popc(is_equal) << 16);
-    const uint32_t upto = warp_scan(mine);
-    uint32_t s = keep_before + ((upto - mine) & 0xFFFFu), q = equal_before + ((upto - mine) >> 16);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t is_s = is_sure >> e & 1u, is_q = is_equal >> e & 1u;
-      if (is_s || (is_q && q < left)) idx[s + min(q, left)] = i + e;
-      s += is_s;
-      q += is_q;
-    }
-    const uint32_t total = __shfl_sync(0xffffffffu, upto, 31);
-    keep_before += total & 0xFFFFu;
-    equal_before += total >> 16;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int i0 = p_begin; i0 < p_end; i0 += 32) {   // (a part is a multiple of 32)
+    const int i = i0 + lane;
+    const uint32_t k = i < p_end ? key_of(i) : 0u;
+    const bool equal_here = k == prefix && i < p_end;
+    const uint32_t is_sure = __ballot_sync(0xffffffffu, k > prefix);
+    const uint32_t is_equal = __ballot_sync(0xffffffffu, equal_here);
+    const uint32_t q = equal_before + __popc(is_equal & below);
+    if (k > prefix || (equal_here && q < left))
+      idx[keep_before + __popc(is_sure & below) + min(q, left)] = i;
+    keep_before += __popc(is_sure);
+    equal_before += __popc(is_equal);
   }
+  // (not earlier: blocks of the gather that waited beside these took 25 us from them)
+  pdl_launch_dependents();
   __syncwarp();
   cluster_sync();   // no block ends while another may read its shared memory
 }
@@ -596,21 +612,25 @@ cudaError_t launch_kv4_rows(bool load, const Kv4RowsLaunch& a, cudaStream_t stre
 
 cudaError_t launch_kv4_evict(const Kv4EvictLaunch& a, cudaStream_t stream) {
   const int pairs = a.B * a.H;
-  // blocks that share a pair: about 8,192 slots of the longest each
-  int cluster = 1, dev = 0;
-  while (cluster < kMaxCluster && a.src_cap > 8192ll * cluster) cluster *= 2;
-  // keys of a whole run where they fit (16,384 leave room for two blocks an SM)
+  // Blocks that share a pair: as many as leave all pairs resident at once (two
+  // blocks an SM: 56 pairs of 104,448 slots take 5 each; 8 took two rounds and
+  // half as long again), but 4,096 slots each at least.  A block holds its keys
+  // where two blocks' fit an SM, else makes them anew each time.
+  int dev = 0;
+  int cluster = std::max(1, std::min(kMaxCluster, 2 * 148 / pairs));
+  cluster = static_cast<int>(std::min<int64_t>(cluster, (a.src_cap + 4095) / 4096));
   const int64_t run = (a.src_cap + 4 * cluster - 1) / (4 * cluster) * 4;
-  const int held = static_cast<int>(run <= kHeldKeys ? run : 0);
+  const bool held = run <= kHeldKeys;
   static PerDeviceOnce once;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess)
     e = once.run(dev, [] {
-      return cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
+      return cudaFuncSetAttribute(kv4_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
     });
   if (e != cudaSuccess) return e;
-  e = launch_after(kv4_select_kernel, dim3(static_cast<unsigned>(pairs) * cluster), kSelThreads, held * 4, cluster,
-                   stream, a, cluster, held);
+  e = launch_after(held ? kv4_select_kernel<true> : kv4_select_kernel<false>,
+                   dim3(static_cast<unsigned>(pairs) * cluster), kSelThreads, held ? run * 4 : 0, cluster, stream, a,
+                   cluster);
   if (e != cudaSuccess) return e;
   const int64_t most = a.keep < a.src_cap ? a.keep : a.src_cap;
   return launch_after(kv4_gather_kernel,
