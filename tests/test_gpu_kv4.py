@@ -315,6 +315,78 @@ def test_attention_of_a_ragged_batch(gpu):
     _run_attn(gpu, lens, 2, 2, 1, 2048, 80, weights=True)
 
 
+@pytest.mark.parametrize("B", [33, 70, 130])
+def test_attention_of_many_sequences(gpu, B):
+    """More sequences than a warp looks through at once, most of them short, some empty."""
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.choice([0, 0, 1, 5, 31, 128, 129, 200], B)]
+    _run_attn(gpu, lens, 1, 1, 1, 224, 82 + B, weights=True)
+    _run_attn(gpu, lens, 1, 3, 1, 224, 83 + B)
+
+
+def test_the_largest_batch(gpu):
+    """1,024 sequences, three of them with tokens: append, attention and load find them."""
+    import torch
+    B = 1024
+    lens = [0] * B
+    lens[0], lens[511], lens[1023] = 3, 70, 33
+    kv, cache, k, v = _make(gpu, lens, 1, 96, 84)
+    host = _host(kv, cache)
+    back_k, back_v = torch.zeros_like(k), torch.zeros_like(v)
+    U.ulysses_kv4_load(kv, cache, back_k, back_v, _i32(_cu(lens), gpu), _i32([0] * B, gpu))
+    g = torch.Generator(device=gpu)
+    g.manual_seed(85)
+    q = torch.randn((B, 1, 1, D), generator=g, device=gpu).to(torch.bfloat16)
+    out = torch.full_like(q, 4.0)
+    ws = torch.empty(kv.workspace_bytes(1, 1), dtype=torch.uint8, device=gpu)
+    U.ulysses_kv4_attn(kv, cache, q, out, _i32(lens, gpu), SCALE, workspace=ws)
+    at = 0
+    for b in (0, 511, 1023):
+        n = lens[b]
+        want, _ = host.values(b, 0, 0, n, 0)
+        assert np.array_equal(_bits(back_k[at:at + n, 0]), orc.f64_to_bf16(want))
+        v64, vs = host.values(b, 0, 0, n, 1)
+        o, _, p = orc.attention(_f64(q)[b, 0, 0], want, v64, SCALE)
+        assert np.all(np.abs(_f64(out)[b, 0, 0] - o) <= bound(_f64(q)[b, 0, 0], want, v64, vs, SCALE, o, p))
+        at += n
+    rest = [b for b in range(B) if not lens[b]]
+    assert not bool(out[rest].any())
+    assert U.ulysses_kv4_last_device_error(kv) == 0
+
+
+def test_attention_of_constant_rows(gpu):
+    """Steps of 0: a slot's rows are their minima, and the codes do not count."""
+    import torch
+    n = 150
+    kv = U.ulysses_kv4_plan(1, 2, D, 160)
+    cache = torch.zeros(kv.cache_bytes, dtype=torch.uint8, device=gpu)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(86)
+    k = torch.randn((n, 2, 2, 1), generator=g, device=gpu).expand(n, 2, 2, 64).reshape(n, 2, D).to(torch.bfloat16)
+    v = torch.randn((n, 2, 2, 1), generator=g, device=gpu).expand(n, 2, 2, 64).reshape(n, 2, D).to(torch.bfloat16)
+    v[:, 1] = 0
+    U.ulysses_kv4_append(kv, cache, k, v, _i32([0, n], gpu), _i32([0], gpu))
+    q = torch.randn((1, 1, 2, D), generator=g, device=gpu).to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty((1, 2, 1), device=gpu)
+    ws = torch.empty(kv.workspace_bytes(2, 1), dtype=torch.uint8, device=gpu)
+    U.ulysses_kv4_attn(kv, cache, q, out, _i32([n], gpu), SCALE, lse=lse, workspace=ws)
+    _check_attn(kv, _host(kv, cache), q, out, lse, [n], False)
+    assert not bool(out[0, 0, 1].any())
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 50.0])
+def test_attention_scales(gpu, scale):
+    import torch
+    kv, cache, _, _ = _make(gpu, [300], 2, 320, 87)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(88)
+    q = torch.randn((1, 1, 10, D), generator=g, device=gpu).to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty((1, 10, 1), device=gpu)
+    ws = torch.empty(kv.workspace_bytes(10, 1), dtype=torch.uint8, device=gpu)
+    U.ulysses_kv4_attn(kv, cache, q, out, _i32([300], gpu), scale, lse=lse, workspace=ws)
+    _check_attn(kv, _host(kv, cache), q, out, lse, [300], False, scale=scale)
+
+
 def test_attention_split_over_every_cta(gpu):
     """One pair, more tiles than CTAs: every CTA leaves a part."""
     _run_attn(gpu, [80_001], 1, 1, 1, 80_032, 81, weights=True)
@@ -451,6 +523,60 @@ def test_eviction_keeps_the_heaviest_slots(gpu, kind, lens, keep, sink, recent):
     assert U.ulysses_kv4_last_device_error(kv) == 0
     assert torch.equal(cache, source)
     _check_evict(kv, cache, dst_kv, dst, before, lens, new, keep, sink, recent)
+
+
+@pytest.mark.parametrize("keep", [150, 160, 170, 199])
+def test_eviction_whose_border_is_among_nan(gpu, keep):
+    """A fifth of the weights are NaN, so the last kept slots are the lowest of those."""
+    import torch
+    rng = np.random.default_rng(keep)
+    kv, cache, _, _ = _make(gpu, [200, 198], 3, 224, 21)
+    w = rng.random((2, 3, 224), dtype=np.float32)
+    w[rng.random(w.shape) < 0.2] = np.nan
+    at = kv.weight_offset
+    cache[at:at + 4 * w.size].view(torch.float32).copy_(torch.from_numpy(w).to(gpu).view(-1))
+    dst_kv = U.ulysses_kv4_plan(2, 3, D, 256)
+    dst = torch.zeros(dst_kv.cache_bytes, dtype=torch.uint8, device=gpu)
+    before, new = dst.clone(), _i32([0, 0], gpu)
+    U.ulysses_kv4_evict(kv, cache, dst_kv, dst, _i32([200, 198], gpu), new, keep)
+    _check_evict(kv, cache, dst_kv, dst, before, [200, 198], new, keep, 0, 0)
+
+
+def test_eviction_into_a_larger_cache_and_of_lengths_outside(gpu):
+    import torch
+    kv, cache, _, _ = _make(gpu, [60, 64, 10], 2, 64, 22)
+    dst_kv = U.ulysses_kv4_plan(3, 2, D, 128)
+    dst = torch.full((dst_kv.cache_bytes,), 0x11, dtype=torch.uint8, device=gpu)
+    before, new = dst.clone(), _i32([0, 0, 0], gpu)
+    U.ulysses_kv4_evict(kv, cache, dst_kv, dst, _i32([60, 64, 10], gpu), new, 100, 10, 10)
+    _check_evict(kv, cache, dst_kv, dst, before, [60, 64, 10], new, 100, 10, 10)
+    assert U.ulysses_kv4_last_device_error(kv) == 0
+    dst.copy_(before)
+    U.ulysses_kv4_evict(kv, cache, dst_kv, dst, _i32([-1, 1 << 30, 10], gpu), new, 20)
+    assert U.ulysses_kv4_last_device_error(kv) == 16
+    _check_evict(kv, cache, dst_kv, dst, before, [0, 64, 10], new, 20, 0, 0)
+
+
+def test_eviction_of_more_keys_than_a_block_holds(gpu):
+    """150 pairs, so that one block has a pair's 23,000 slots and makes the keys anew each time."""
+    import torch
+    B, n, keep, cap = 150, 23_000, 1_000, 23_008
+    kv = U.ulysses_kv4_plan(B, 1, D, cap)
+    cache = torch.zeros(kv.cache_bytes, dtype=torch.uint8, device=gpu)
+    rng = np.random.default_rng(23)
+    w = (rng.integers(0, 5000, (B, cap)) / 64).astype(np.float32)
+    at = kv.weight_offset
+    cache[at:at + 4 * w.size].view(torch.float32).copy_(torch.from_numpy(w).to(gpu).view(-1))
+    at = kv.position_offset
+    cache[at:].view(torch.int32).copy_(torch.arange(cap, dtype=torch.int32, device=gpu).repeat(B))
+    dst_kv = U.ulysses_kv4_plan(B, 1, D, 1024)
+    dst = torch.zeros(dst_kv.cache_bytes, dtype=torch.uint8, device=gpu)
+    new = torch.zeros(B, dtype=torch.int32, device=gpu)
+    lens = [n - b for b in range(B)]
+    U.ulysses_kv4_evict(kv, cache, dst_kv, dst, _i32(lens, gpu), new, keep, 4, 100)
+    got = _host(dst_kv, dst)
+    for b in (0, 1, 2, 3, 77, 148, 149):
+        assert np.array_equal(got.pos[b, 0, :keep], orc.kept_slots(w[b], lens[b], keep, 4, 100)), b
 
 
 @pytest.mark.parametrize("kind", ["spread", "ties"])
@@ -636,6 +762,68 @@ def test_a_captured_decoding_loop(gpu):
         assert torch.equal(out, want[i]), i
     assert torch.equal(cache, direct)
     assert U.ulysses_kv4_last_device_error(kv) == 0
+
+
+def test_a_captured_eviction(gpu):
+    """Eviction and load in a graph; a replay goes by the lengths and weights of its time."""
+    import torch
+    kv, cache, _, _ = _make(gpu, [90, 40], 2, 96, 72)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(73)
+    n = 2 * 2 * 96
+    w = cache[kv.weight_offset:kv.weight_offset + 4 * n].view(torch.float32)
+    dst_kv = U.ulysses_kv4_plan(2, 2, D, 64)
+    dst = torch.zeros(dst_kv.cache_bytes, dtype=torch.uint8, device=gpu)
+    lengths, new = _i32([90, 40], gpu), _i32([0, 0], gpu)
+    cu, start = _i32([0, 50, 90], gpu), _i32([0, 0], gpu)
+    k, v = (torch.zeros((90, 2, D), dtype=torch.bfloat16, device=gpu) for _ in range(2))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        U.ulysses_kv4_evict(kv, cache, dst_kv, dst, lengths, new, 50, 2, 7)
+        U.ulysses_kv4_load(dst_kv, dst, k, v, cu, start)
+    for lens in ([90, 40], [60, 96], [3, 50]):
+        w.copy_(torch.rand(n, generator=g, device=gpu))
+        lengths.copy_(_i32(lens, gpu))
+        before = dst.clone()
+        graph.replay()
+        _check_evict(kv, cache, dst_kv, dst, before, lens, new, 50, 2, 7)
+        host = _host(dst_kv, dst)
+        want, _ = host.values(0, 1, 0, 50, 0)
+        assert np.array_equal(_bits(k[:50, 1]), orc.f64_to_bf16(want))
+
+
+def test_strides_of_single_rows_and_heads_do_not_count(gpu):
+    import torch
+    kv, cache, k, v = _make(gpu, [40], 1, 64, 96)
+    row = torch.randn(2, 1, 1, D, device=gpu).to(torch.bfloat16)
+    odd = [torch.as_strided(row[i], (1, 1, D), (3, 5, 1), row[i].storage_offset()) for i in range(2)]
+    U.ulysses_kv4_append(kv, cache, odd[0], torch.as_strided(odd[1], (1, 1, D), (7, 1, 1), odd[1].storage_offset()),
+                         _i32([0, 1], gpu), _i32([40], gpu))
+    _check_append(kv, cache, row[0], row[1], [1], [40])
+    q = torch.as_strided(row, (1, 1, 1, D), (1, 3, 5, 1))
+    out = torch.empty((1, 1, 1, D), dtype=torch.bfloat16, device=gpu)
+    ws = torch.empty(kv.workspace_bytes(1, 1), dtype=torch.uint8, device=gpu)
+    U.ulysses_kv4_attn(kv, cache, q, out, _i32([41], gpu), SCALE, workspace=ws)
+    _check_attn(kv, _host(kv, cache), q, out, None, [41], False)
+
+
+def test_append_repeats_a_row_that_heads_share(gpu):
+    """A head stride of 0: one K/V row for all heads."""
+    import torch
+    kv = U.ulysses_kv4_plan(1, 6, D, 32)
+    cache = torch.zeros(kv.cache_bytes, dtype=torch.uint8, device=gpu)
+    k = torch.randn((9, 1, D), device=gpu).to(torch.bfloat16).expand(9, 6, D)
+    v = torch.randn((9, 1, D), device=gpu).to(torch.bfloat16).expand(9, 6, D)
+    U.ulysses_kv4_append(kv, cache, k, v, _i32([0, 9], gpu), _i32([3], gpu))
+    _check_append(kv, cache, k, v, [9], [3])
+    # a rank stride of 0: the same two heads for all three ranks
+    two = torch.randn((2, 1, 9, 2, D), device=gpu).to(torch.bfloat16).expand(2, 3, 9, 2, D)
+    U.ulysses_kv4_append(kv, cache, two[0], two[1], _i32([0, 9], gpu), _i32([12], gpu))
+    flat = two.permute(0, 2, 1, 3, 4).reshape(2, 9, 6, D)
+    _check_append(kv, cache, flat[0], flat[1], [9], [12])
+    with pytest.raises(U.UlyssesError):
+        U.ulysses_kv4_load(kv, cache, k, v, _i32([0, 9], gpu), _i32([3], gpu))
 
 
 def test_two_calls_at_once_on_two_streams(gpu):

@@ -30,6 +30,8 @@ def test_plan_refusals():
     assert _code(1, 1025, 128, 32) == _lib.ULYSSES_ERR_UNSUPPORTED
     assert _code(1024, 64, 128, 32) == _lib.ULYSSES_ERR_UNSUPPORTED
     assert _code(1, 1, 128, 1 << 31) == _lib.ULYSSES_ERR_UNSUPPORTED
+    assert _code((1 << 32) + 1, 1, 128, 32) == _lib.ULYSSES_ERR_UNSUPPORTED      # no wrapping into an int32
+    assert _code(1, -(1 << 32) + 1, 128, 32) == _lib.ULYSSES_ERR_ARG
     assert U.load().ulysses_kv4_plan(None, 1, 1, 128, 32) == _lib.ULYSSES_ERR_ARG
 
 

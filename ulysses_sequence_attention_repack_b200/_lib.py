@@ -512,7 +512,7 @@ class KV4Plan:
 
     def workspace_bytes(self, q_heads: int, q_len: int, weights: bool = False) -> int:
         """Workspace of ulysses_kv4_attn."""
-        return load().ulysses_kv4_attn_workspace_bytes(self.handle, int(q_heads), int(q_len),
+        return load().ulysses_kv4_attn_workspace_bytes(self.handle, _kv4_int(q_heads), _kv4_int(q_len),
                                                        ULYSSES_KV4_WEIGHTS if weights else 0)
 
     def destroy(self) -> None:
@@ -531,7 +531,7 @@ def ulysses_kv4_plan(batch: int, heads: int, D: int, capacity: int) -> KV4Plan:
     """The geometry of 4-bit K/V caches: `capacity` slots (a multiple of 32)
     for each of `batch` sequences and `heads` K/V heads of D = 128."""
     h = ctypes.c_void_p()
-    _check(load().ulysses_kv4_plan(ctypes.byref(h), int(batch), int(heads), int(D), int(capacity)),
+    _check(load().ulysses_kv4_plan(ctypes.byref(h), _kv4_int(batch), _kv4_int(heads), _kv4_int(D), int(capacity)),
            "ulysses_kv4_plan")
     return KV4Plan(h.value, int(batch), int(heads), int(D), int(capacity))
 
@@ -575,6 +575,15 @@ def _kv4_cache(where: str, name: str, kv: KV4Plan, x, t: dict):
     return _kv4_flat(where, name, x, t["tensor"], t["uint8"], kv.cache_bytes, dev), dev
 
 
+def _kv4_strides(shape, stride) -> tuple:
+    return tuple(0 if n == 1 else d for n, d in zip(shape, stride))
+
+
+def _kv4_int(x) -> int:
+    """An int32 argument; what is outside int32 becomes its end, which the library refuses."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
+
+
 def _kv4_rows(where: str, kv: KV4Plan, cache, k, v, cu, start, t: dict):
     """The common arguments of append and load: K and V of one shape and
     layout, [rows, heads, D] or, split over ranks, [P, rows, heads / P, D]."""
@@ -586,11 +595,16 @@ def _kv4_rows(where: str, kv: KV4Plan, cache, k, v, cu, start, t: dict):
         if x.get_device() != dev:
             raise ValueError(f"{where}: {name} is not on the current device")
     shape, stride = k.shape, k.stride()
-    if shape != v.shape or stride != v.stride():
-        raise ValueError(f"{where}: k and v must have one shape and layout")
     n = len(shape)
     if n not in (3, 4) or shape[-1] != kv.D or stride[-1] != 1:
         raise ValueError(f"{where}: k and v are [rows, heads, {kv.D}] or [ranks, rows, heads / ranks, {kv.D}]")
+    if 1 in shape:   # the stride of a single row or head says nothing
+        stride = _kv4_strides(shape, stride)
+        same = v.shape == shape and stride == _kv4_strides(shape, v.stride())
+    else:
+        same = v.shape == shape and v.stride() == stride
+    if not same:
+        raise ValueError(f"{where}: k and v must have one shape and layout")
     ranks, rank_stride = (shape[0], stride[0]) if n == 4 else (1, 0)
     if ranks * shape[-2] != kv.heads:
         raise ValueError(f"{where}: {ranks * shape[-2]} heads, the plan has {kv.heads}")
@@ -643,6 +657,7 @@ def ulysses_kv4_attn(kv: KV4Plan, cache, q, out, lengths, softmax_scale: float, 
     B, q_len, q_heads, D = shape
     if q_len > 1 and B > 1 and stride[0] != q_len * stride[1]:
         raise ValueError(f"{where}: the rows of q must be evenly spaced over sequences and queries")
+    token_stride = stride[1] if q_len > 1 else (stride[0] if B > 1 else 0)
     o = _kv4_flat(where, "out", out, T, t["bf16"], B * q_len * q_heads * D, dev)
     if out.shape != shape:
         raise ValueError(f"{where}: out has q's shape")
@@ -650,8 +665,8 @@ def ulysses_kv4_attn(kv: KV4Plan, cache, q, out, lengths, softmax_scale: float, 
     ws, nbytes = None, 0
     if workspace is not None:
         ws, nbytes = _kv4_flat(where, "workspace", workspace, T, t["uint8"], 0, dev), workspace.numel()
-    _check(load().ulysses_kv4_attn(kv.handle, c, q.data_ptr(), q_heads, q_len, stride[1] if q_len > 1 else stride[0],
-                                   stride[2], o, ls, _kv4_flat(where, "lengths", lengths, T, t["int32"], B, dev),
+    _check(load().ulysses_kv4_attn(kv.handle, c, q.data_ptr(), q_heads, q_len, token_stride,
+                                   stride[2] if q_heads > 1 else 0, o, ls, _kv4_flat(where, "lengths", lengths, T, t["int32"], B, dev),
                                    softmax_scale,
                                    (ULYSSES_KV4_CAUSAL if causal else 0) | (ULYSSES_KV4_WEIGHTS if weights else 0),
                                    ws, nbytes, _kv4_stream(stream, t)), where)
@@ -669,7 +684,7 @@ def ulysses_kv4_evict(src_kv: KV4Plan, src_cache, dst_kv: KV4Plan, dst_cache, le
     _check(load().ulysses_kv4_evict(src_kv.handle, src, dst_kv.handle, dst,
                                     _kv4_flat(where, "lengths", lengths, T, i32, src_kv.batch, dev),
                                     _kv4_flat(where, "new_lengths", new_lengths, T, i32, src_kv.batch, dev),
-                                    keep, sink, recent, _kv4_stream(stream, t)), where)
+                                    _kv4_int(keep), _kv4_int(sink), _kv4_int(recent), _kv4_stream(stream, t)), where)
 
 
 def ulysses_kv4_last_device_error(kv: KV4Plan, stream=None) -> int:

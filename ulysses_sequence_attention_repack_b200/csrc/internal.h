@@ -170,9 +170,11 @@ struct Kv4RowsLaunch {
   int32_t* pos;
   int64_t blocks_bytes;     // extent of the blocks, for the bounds-checked build
   unsigned int* err;
+  uint32_t items;           // set by the launch: warps with work, and r.rows
+  int32_t rows32;
 };
 
-cudaError_t launch_kv4_rows(bool load, const Kv4RowsLaunch& a, cudaStream_t stream);
+cudaError_t launch_kv4_rows(bool load, Kv4RowsLaunch a, cudaStream_t stream);
 
 struct Kv4EvictLaunch {
   int32_t B, H;

@@ -210,7 +210,7 @@ static int check_attn_shape(const ulysses_kv4_t* kv, int32_t q_heads, int32_t q_
   const int64_t R = static_cast<int64_t>(q_heads / kv->H) * q_len;
   if (R > kMaxInt32 / pairs) return ULYSSES_ERR_UNSUPPORTED;
   const int64_t tiles = (kv->cap + 127) / 128 * pairs;   // < 2^24 * 2^16
-  if (tiles > kMaxInt32 / ((R + 7) / 8)) return ULYSSES_ERR_UNSUPPORTED;
+  if (tiles > kMaxInt32 / 2 / ((R + 7) / 8)) return ULYSSES_ERR_UNSUPPORTED;
   return ULYSSES_OK;
 }
 

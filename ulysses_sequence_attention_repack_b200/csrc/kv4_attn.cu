@@ -246,12 +246,23 @@ __device__ __forceinline__ void finish_row(const Args& a, int b, int h, int r, i
 // Dynamic shared memory: the warps' rings, then their sums [warp][row][128],
 // maxima and sums of p [warp][row].
 __host__ __device__ inline int smem_rows(int R, int RPB) { return R < RPB ? R : RPB; }
-__host__ __device__ inline int64_t smem_bytes(int R, int RPB) {
-  return kWarps * (kStages * kKv4BlockBytes + smem_rows(R, RPB) * (kKv4Dim * 4 + 8));
+// Then a warp's scratch: with kR > 0 its products' results [slot][row][group] in
+// fp32, p s of a block [row][group][32 slots] in fp16 and 16 bytes of zeros;
+// else a block's K scales and minima, and V's, 16 bytes a slot.
+__host__ __device__ constexpr int scratch_bytes(int kR) { return kR ? kR * (256 + 128) + 16 : 1024; }
+__host__ __device__ inline int64_t smem_bytes(int R, int RPB, int kR) {
+  return kWarps * (kStages * kKv4BlockBytes + smem_rows(R, RPB) * (kKv4Dim * 4 + 8) + scratch_bytes(kR));
 }
 
-template <int NT, bool kWeights>
+// NT: 8 or 16 query rows in a product.  kR: with 1 or 2 rows most columns of
+// z^T are empty, so its lanes would spend the softmax's instructions on
+// nothing; then z^T goes through shared memory and a lane takes one slot and
+// its kR rows (0: more rows; a lane takes 4 slots and 2 rows as the products
+// leave them).  104,448 slots x 56 heads: 1 row 164 -> 141 us, 2 rows 164 -> 148;
+// with 4 rows it gains nothing (164 -> 167).
+template <int NT, int kR, bool kWeights>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(const Args a) {
+  static_assert(kR == 0 || NT == 1, "few rows are one product wide");
   constexpr int RPB = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bar_mem[kWarps][kStages];
@@ -263,8 +274,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
   float* mo = reinterpret_cast<float*>(smem + kWarps * kStages * kKv4BlockBytes);   // [warp][mrows][128]
   float* mM = mo + kWarps * mrows * kKv4Dim;
   float* ml = mM + kWarps * mrows;
+  constexpr int kRows = kR ? kR : 1;
+  uint8_t* zbuf = reinterpret_cast<uint8_t*>(ml + kWarps * mrows) + warp * scratch_bytes(kR);   // [slot][row][group] fp32
+  uint8_t* wbuf = zbuf + kRows * 256;                                                           // [row][group][slot] fp16
+  float4* kput = reinterpret_cast<float4*>(zbuf);
+  // this lane's column of p s as the second operand (all 32 slots of row g), or zeros
+  const uint8_t* wcol = g < kR ? wbuf + g * 128 + t * 16 : wbuf + kRows * 128;
+  const int wstep = g < kR ? 64 : 0;
+  // slot `lane`: pair (slot & 7) / 2 of register 2 (slot / 16) + (slot / 8 & 1) of a column
+  uint8_t* wput = wbuf + ((lane & 7) >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;
+  if (kR && lane < 4) reinterpret_cast<uint32_t*>(wbuf + kRows * 128)[lane] = 0u;
 
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     abort_mem = drain_mem = 0;
     for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&bar_mem[0][0]) + 8 * i, 1);
@@ -312,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
     float qscale[NT][2], qsum[NT][2][2];
     int limit[NT][2];
     int lowest = len;
+    float rq[kRows], rq0[kRows], rq1[kRows];   // kR: scale and group sums of every row, and its limit
+    int rlimit[kRows];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + 8 * nt + g;
@@ -381,6 +403,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
         limit[nt][c] = rr < a.R ? (a.causal ? max(0, len - a.Lq + rr / a.G + 1) : len) : 0;
         if (rr < a.R) lowest = min(lowest, limit[nt][c]);
       }
+      if constexpr (kR > 0) {
+#pragma unroll
+        for (int rr = 0; rr < kR; ++rr) {
+          rq[rr] = __shfl_sync(0xffffffffu, qs, 4 * rr);
+          rq0[rr] = __shfl_sync(0xffffffffu, sum[0], 4 * rr);
+          rq1[rr] = __shfl_sync(0xffffffffu, sum[1], 4 * rr);
+          rlimit[rr] = rr < a.R ? (a.causal ? max(0, len - a.Lq + rr / a.G + 1) : len) : 0;
+        }
+      }
     }
     lowest = __reduce_min_sync(0xffffffffu, lowest);
 
@@ -401,144 +432,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       }
     }
 
-    // One block of 32 slots at blk.  kEdge: some row does not see all of them.
-    auto step = [&](auto edge_tag, const uint8_t* blk, int slot0) {
-      constexpr bool kEdge = decltype(edge_tag)::value;
-      uint4 meta[2][2];
-      float s[NT][2][4];   // z log2 e: [16-slot half][slot g row 2t, g 2t+1, g+8 2t, g+8 2t+1]
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const uint4 ka = *reinterpret_cast<const uint4*>(blk + (16 * mt + g) * 64 + t * 16);
-        const uint4 kb = *reinterpret_cast<const uint4*>(blk + (16 * mt + g + 8) * 64 + t * 16);
-        meta[mt][0] = *reinterpret_cast<const uint4*>(blk + kKv4MetaOffset + (16 * mt + g) * 16);
-        meta[mt][1] = *reinterpret_cast<const uint4*>(blk + kKv4MetaOffset + (16 * mt + g + 8) * 16);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-        float d[NT][2][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) d[nt][0][c] = d[nt][1][c] = 0.f;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const uint32_t xa = wa[v] >> 8, xb = wb[v] >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma(d[nt][v & 1], wa[v] & kLow, wb[v] & kLow, wa[v] & kHigh, wb[v] & kHigh, qf[nt][4 * v],
-                qf[nt][4 * v + 1]);
-            mma(d[nt][v & 1], xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[nt][4 * v + 2], qf[nt][4 * v + 3]);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4& m = meta[mt][c >> 1];
-            const int row = c & 1;
-            float x = bf16_lo(m.x) * d[nt][0][c];
-            x = fmaf(bf16_hi(m.x), qsum[nt][row][0], x);
-            x = fmaf(bf16_lo(m.y), d[nt][1][c], x);
-            x = fmaf(bf16_hi(m.y), qsum[nt][row][1], x);
-            x *= qscale[nt][row];
-            const int slot = slot0 + 16 * mt + g + 8 * (c >> 1);
-            if (kEdge && slot >= limit[nt][row]) x = NEG_INF;
-            s[nt][mt][c] = x;
-            if (kWeights) {
-              const int r = row0 + 8 * nt + 2 * t + row;
-              if (r < a.R && (!kEdge || slot < len)) a.logits[(bh * a.R + r) * a.cap + slot] = x;
-            }
-          }
-      }
-      // slots behind the length hold anything: nothing of them may reach a sum
-      if (kEdge) {
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (slot0 + 16 * mt + g + 8 * i >= len) meta[mt][i] = make_uint4(0, 0, 0, 0);
-      }
-      float vs[2][2][2];   // V scales [half][slot g, g + 8][group]
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          vs[mt][i][0] = bf16_lo(meta[mt][i].z);
-          vs[mt][i][1] = bf16_lo(meta[mt][i].w);
-        }
-      float top[NT][2];
-      bool move = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          top[nt][c] = fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2]));
-          move |= top[nt][c] > M[nt][c] + kGrow;
-        }
-      float big[2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        big[w] = fmaxf(fmaxf(vs[0][0][w], vs[0][1][w]), fmaxf(vs[1][0][w], vs[1][1][w]));
-        move |= big[w] > s_limit[w];
-      }
-      if (__any_sync(0xffffffffu, move)) {
-        float down[2];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          // scales are not negative, so their bits order them
-          const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(big[w]));
-          const int c_new = max(c_exp[w], max(-100, min(100, static_cast<int>(m >> 23) - 127)));
-          down[w] = ex2(static_cast<float>(c_exp[w] - c_new));
-          c_exp[w] = c_new;
-          s_limit[w] = pow2(c_new + 2);
-          s_up[w] = pow2(kHeadroom - c_new);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float m = top[nt][c];
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float m_new = fmaxf(M[nt][c], m);
-            const float al = m_new == M[nt][c] ? 1.f : ex2(M[nt][c] - m_new);
-            M[nt][c] = m_new;
-            Ms[nt][c] = m_new == NEG_INF ? 0.f : m_new;
-            l[nt][c] *= al;
-            z0[nt][c][0] *= al;
-            z0[nt][c][1] *= al;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              acc[nt][i][c] *= al * down[i >> 2];
-              acc[nt][i][c + 2] *= al * down[i >> 2];
-            }
-          }
-      }
-      // p, its sums, and p s as the operand of the second product
-      uint32_t pb[2][NT][2][2];   // [group][row block][half][operand register]
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          float w0[4], w1[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int i = c >> 1, row = c & 1;
-            const float p = ex2(s[nt][mt][c] - Ms[nt][row]);
-            l[nt][row] += p;
-            const uint4& m = meta[mt][i];
-            w0[c] = p * (vs[mt][i][0] * s_up[0]);
-            w1[c] = p * (vs[mt][i][1] * s_up[1]);
-            float m0 = bf16_hi(m.z), m1 = bf16_hi(m.w);
-            if (kEdge && slot0 + 16 * mt + g + 8 * i >= limit[nt][row]) w0[c] = w1[c] = m0 = m1 = 0.f;
-            z0[nt][row][0] = fmaf(p, m0, z0[nt][row][0]);
-            z0[nt][row][1] = fmaf(p, m1, z0[nt][row][1]);
-          }
-          pb[0][nt][mt][0] = transpose8x8(pack_f16(w0[0], w0[1]));
-          pb[0][nt][mt][1] = transpose8x8(pack_f16(w0[2], w0[3]));
-          pb[1][nt][mt][0] = transpose8x8(pack_f16(w1[0], w1[1]));
-          pb[1][nt][mt][1] = transpose8x8(pack_f16(w1[2], w1[3]));
-        }
-      // o^T += V^T p^T: this lane holds dims 8g .. 8g + 7 of each group, and
+    // o^T += V^T p^T for the p s of a block
+    uint32_t pb[2][NT][2][2];   // [group][row block][half][operand register]
+    auto values = [&](const uint8_t* blk) {
+      // this lane holds dims 8g .. 8g + 7 of each group, and
       // slots 2t, 2t + 1 and 2t + 8, 2t + 9 of the half are the pairs of its registers
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
@@ -565,6 +462,248 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       }
     };
 
+    float rM[kRows], rMs[kRows], rl[kRows], rz[kRows][2];   // kR: the same of every row; sums over this lane's slots
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      rM[r] = NEG_INF;
+      rMs[r] = rl[r] = rz[r][0] = rz[r][1] = 0.f;
+    }
+
+    // The powers of two of the scales, replaced because a slot's (each lane one) outgrew them: *down what that makes of
+    // finished sums.
+    auto grow_scales = [&](const float (&vs)[2], float (&down)[2]) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(vs[w]));   // (scales are not negative)
+        const int c_new = max(c_exp[w], max(-100, min(100, static_cast<int>(big >> 23) - 127)));
+        down[w] = ex2(static_cast<float>(c_exp[w] - c_new));
+        c_exp[w] = c_new;
+        s_limit[w] = pow2(c_new + 2);
+        s_up[w] = pow2(kHeadroom - c_new);
+      }
+    };
+
+    // One block, a slot a lane.
+    auto step_few = [&](auto edge_tag, const uint8_t* blk, int slot0) {
+      constexpr bool kEdge = decltype(edge_tag)::value;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint4 ka = *reinterpret_cast<const uint4*>(blk + (16 * mt + g) * 64 + t * 16);
+        const uint4 kb = *reinterpret_cast<const uint4*>(blk + (16 * mt + g + 8) * 64 + t * 16);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        float d[2][4] = {};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t xa = wa[v] >> 8, xb = wb[v] >> 8;
+          mma(d[v & 1], wa[v] & kLow, wb[v] & kLow, wa[v] & kHigh, wb[v] & kHigh, qf[0][4 * v], qf[0][4 * v + 1]);
+          mma(d[v & 1], xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[0][4 * v + 2], qf[0][4 * v + 3]);
+        }
+        if (2 * t < kR) {   // the lanes with columns of rows
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint8_t* to = zbuf + (16 * mt + g + 8 * i) * (8 * kRows) + t * 16;
+            if constexpr (kR == 1)
+              *reinterpret_cast<float2*>(to) = make_float2(d[0][2 * i], d[1][2 * i]);
+            else
+              *reinterpret_cast<float4*>(to) = make_float4(d[0][2 * i], d[1][2 * i], d[0][2 * i + 1], d[1][2 * i + 1]);
+          }
+        }
+      }
+      __syncwarp();
+      const int slot = slot0 + lane;
+      uint4 m = *reinterpret_cast<const uint4*>(blk + kKv4MetaOffset + lane * 16);
+      if (kEdge && slot >= len) m = make_uint4(0, 0, 0, 0);   // anything may be held there
+      const float vs[2] = {bf16_lo(m.z), bf16_lo(m.w)}, vm[2] = {bf16_hi(m.z), bf16_hi(m.w)};
+      float z[kRows];
+      bool move = vs[0] > s_limit[0] || vs[1] > s_limit[1];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float2 d = *reinterpret_cast<const float2*>(zbuf + lane * (8 * kRows) + r * 8);
+        float x = bf16_lo(m.x) * d.x;
+        x = fmaf(bf16_hi(m.x), rq0[r], x);
+        x = fmaf(bf16_lo(m.y), d.y, x);
+        x = fmaf(bf16_hi(m.y), rq1[r], x);
+        x *= rq[r];
+        if (kEdge && slot >= rlimit[r]) x = NEG_INF;
+        z[r] = x;
+        move |= x > rM[r] + kGrow;
+        if (kWeights && r < a.R && (!kEdge || slot < len)) a.logits[(bh * a.R + r) * a.cap + slot] = x;
+      }
+      if (__any_sync(0xffffffffu, move)) {
+        float down[2];
+        grow_scales(vs, down);
+        float al[2] = {1.f, 1.f};   // of this lane's columns of o^T
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          float top = z[r];
+#pragma unroll
+          for (int dlt = 16; dlt; dlt >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, dlt));
+          const float m_new = fmaxf(rM[r], top);
+          const float f = m_new == rM[r] ? 1.f : ex2(rM[r] - m_new);
+          rM[r] = m_new;
+          rMs[r] = m_new == NEG_INF ? 0.f : m_new;
+          rl[r] *= f;
+          rz[r][0] *= f;
+          rz[r][1] *= f;
+          if (t == (r >> 1)) al[r & 1] = f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[0][i][c] *= al[c & 1] * down[i >> 2];
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float p = ex2(z[r] - rMs[r]);
+        rl[r] += p;
+        float w0 = p * (vs[0] * s_up[0]), w1 = p * (vs[1] * s_up[1]);
+        const bool unseen = kEdge && slot >= rlimit[r];   // (whatever this slot's scales are)
+        if (unseen) w0 = w1 = 0.f;
+        rz[r][0] = fmaf(p, unseen ? 0.f : vm[0], rz[r][0]);
+        rz[r][1] = fmaf(p, unseen ? 0.f : vm[1], rz[r][1]);
+        const uint32_t both = pack_f16(w0, w1);
+        *reinterpret_cast<uint16_t*>(wput + r * 128) = static_cast<uint16_t>(both);
+        *reinterpret_cast<uint16_t*>(wput + r * 128 + 64) = static_cast<uint16_t>(both >> 16);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const uint4 x = *reinterpret_cast<const uint4*>(wcol + w * wstep);
+        pb[w][0][0][0] = x.x;
+        pb[w][0][0][1] = x.y;
+        pb[w][0][1][0] = x.z;
+        pb[w][0][1][1] = x.w;
+      }
+      values(blk);
+    };
+
+    // One block of 32 slots at blk.  kEdge: some row does not see all of them.
+    auto step = [&](auto edge_tag, const uint8_t* blk, int slot0) {
+      constexpr bool kEdge = decltype(edge_tag)::value;
+      // each lane turns one slot's scales and minima into fp32 for all
+      {
+        uint4 m = *reinterpret_cast<const uint4*>(blk + kKv4MetaOffset + lane * 16);
+        // slots behind the length hold anything: nothing of them may reach a sum
+        if (kEdge && slot0 + lane >= len) m = make_uint4(0, 0, 0, 0);
+        const float vs[2] = {bf16_lo(m.z), bf16_lo(m.w)};
+        if (__any_sync(0xffffffffu, vs[0] > s_limit[0] || vs[1] > s_limit[1])) {
+          float down[2];
+          grow_scales(vs, down);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[nt][i][c] *= down[i >> 2];
+        }
+        kput[lane] = make_float4(bf16_lo(m.x), bf16_hi(m.x), bf16_lo(m.y), bf16_hi(m.y));
+        kput[32 + lane] = make_float4(vs[0] * s_up[0], bf16_hi(m.z), vs[1] * s_up[1], bf16_hi(m.w));
+      }
+      __syncwarp();
+      float s[NT][2][4];   // z / qscale: [16-slot half][slot g row 2t, g 2t+1, g+8 2t, g+8 2t+1]
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint4 ka = *reinterpret_cast<const uint4*>(blk + (16 * mt + g) * 64 + t * 16);
+        const uint4 kb = *reinterpret_cast<const uint4*>(blk + (16 * mt + g + 8) * 64 + t * 16);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        float d[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) d[nt][0][c] = d[nt][1][c] = 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t xa = wa[v] >> 8, xb = wb[v] >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(d[nt][v & 1], wa[v] & kLow, wb[v] & kLow, wa[v] & kHigh, wb[v] & kHigh, qf[nt][4 * v],
+                qf[nt][4 * v + 1]);
+            mma(d[nt][v & 1], xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[nt][4 * v + 2], qf[nt][4 * v + 3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 k = kput[16 * mt + g + 8 * i];
+          const int slot = slot0 + 16 * mt + g + 8 * i;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int row = 0; row < 2; ++row) {
+              const int c = 2 * i + row;
+              float x = k.x * d[nt][0][c];
+              x = fmaf(k.y, qsum[nt][row][0], x);
+              x = fmaf(k.z, d[nt][1][c], x);
+              x = fmaf(k.w, qsum[nt][row][1], x);
+              if (kEdge && slot >= limit[nt][row]) x = NEG_INF;
+              s[nt][mt][c] = x;
+              if (kWeights) {
+                const int r = row0 + 8 * nt + 2 * t + row;
+                if (r < a.R && (!kEdge || slot < len)) a.logits[(bh * a.R + r) * a.cap + slot] = x * qscale[nt][row];
+              }
+            }
+        }
+      }
+      float top[NT][2];
+      bool move = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[nt][c] = fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2])) * qscale[nt][c];
+          move |= top[nt][c] > M[nt][c] + kGrow;
+        }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float m = top[nt][c];
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            const float m_new = fmaxf(M[nt][c], m);
+            const float al = m_new == M[nt][c] ? 1.f : ex2(M[nt][c] - m_new);
+            M[nt][c] = m_new;
+            Ms[nt][c] = m_new == NEG_INF ? 0.f : m_new;
+            l[nt][c] *= al;
+            z0[nt][c][0] *= al;
+            z0[nt][c][1] *= al;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[nt][i][c] *= al;
+              acc[nt][i][c + 2] *= al;
+            }
+          }
+      }
+      // p, its sums, and p s as the operand of the second product
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float4 va = kput[32 + 16 * mt + g], vb = kput[32 + 16 * mt + g + 8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w0[4], w1[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = c >> 1, row = c & 1;
+            const float4& v = i ? vb : va;
+            const float p = ex2(fmaf(s[nt][mt][c], qscale[nt][row], -Ms[nt][row]));
+            l[nt][row] += p;
+            w0[c] = p * v.x;
+            w1[c] = p * v.z;
+            float m0 = v.y, m1 = v.w;
+            if (kEdge && slot0 + 16 * mt + g + 8 * i >= limit[nt][row]) w0[c] = w1[c] = m0 = m1 = 0.f;
+            z0[nt][row][0] = fmaf(p, m0, z0[nt][row][0]);
+            z0[nt][row][1] = fmaf(p, m1, z0[nt][row][1]);
+          }
+          pb[0][nt][mt][0] = transpose8x8(pack_f16(w0[0], w0[1]));
+          pb[0][nt][mt][1] = transpose8x8(pack_f16(w0[2], w0[3]));
+          pb[1][nt][mt][0] = transpose8x8(pack_f16(w1[0], w1[1]));
+          pb[1][nt][mt][1] = transpose8x8(pack_f16(w1[2], w1[3]));
+        }
+      }
+      values(blk);
+    };
+
     for (int tl = lo; tl < hi; ++tl) {
       const int slot0 = tl * kTile + warp * kKv4BlockSlots;
       if (slot0 >= len) break;
@@ -575,21 +714,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       }
       ++used;
       const uint8_t* blk = ring + stage * kKv4BlockBytes;
-      if (slot0 + kKv4BlockSlots > lowest)
-        step(std::true_type{}, blk, slot0);
-      else
-        step(std::false_type{}, blk, slot0);
+      if constexpr (kR > 0) {
+        if (slot0 + kKv4BlockSlots > lowest)
+          step_few(std::true_type{}, blk, slot0);
+        else
+          step_few(std::false_type{}, blk, slot0);
+      } else {
+        if (slot0 + kKv4BlockSlots > lowest)
+          step(std::true_type{}, blk, slot0);
+        else
+          step(std::false_type{}, blk, slot0);
+      }
       __syncwarp();   // every lane has read the block before it is replaced
       if (alive) feed.next(a, warp, lane);
     }
 
     // the fragment's sums: over the lanes that hold the same rows, then over the warps
+    if constexpr (kR > 0) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+#pragma unroll
+        for (int dlt = 1; dlt < 32; dlt <<= 1) {
+          rl[r] += __shfl_xor_sync(0xffffffffu, rl[r], dlt);
+          rz[r][0] += __shfl_xor_sync(0xffffffffu, rz[r][0], dlt);
+          rz[r][1] += __shfl_xor_sync(0xffffffffu, rz[r][1], dlt);
+        }
+        if (t == (r >> 1)) {
+          M[0][r & 1] = rM[r];
+          l[0][r & 1] = rl[r];
+          z0[0][r & 1][0] = rz[r][0];
+          z0[0][r & 1][1] = rz[r][1];
+        }
+      }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int dlt = 4; dlt < 32; dlt <<= 1) {
+        for (int dlt = 4; dlt < 32 && kR == 0; dlt <<= 1) {
           l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], dlt);
           z0[nt][c][0] += __shfl_xor_sync(0xffffffffu, z0[nt][c][0], dlt);
           z0[nt][c][1] += __shfl_xor_sync(0xffffffffu, z0[nt][c][1], dlt);
@@ -645,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
     tile += hi - lo;
     if (tile < tile_end) at.next_unit(a);
   }
+  pdl_launch_dependents();   // (not earlier: waiting blocks of the next kernel would hold this one's places)
   // a warp that gave up has copies in flight: wait for them (again with a limit) before the memory is freed
   if (!alive) {
     const WaitGuard drain{&drain_mem, a.err, kWaitLimitNs};
@@ -657,15 +821,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kWeightSlots = kJoinThreads * 4;   // slots of a block that adds weights
+constexpr int kWeightSlots = kJoinThreads * 8;   // slots of a block that adds weights
 
 // The parts that one unit's tiles were cut into: those of CTAs c0 .. c1.  A
 // unit that one CTA held is whole.
 struct Parts {
   int c0, c1, chunk, t0;
-  __device__ __forceinline__ void find(const Args& a, int ctas, int b, int unit, int ntiles) {
-    chunk = tiles_per_cta(total_tiles(a, false), ctas);
-    t0 = first_tile(a, b) + unit * ntiles;
+  bool empty;   // no tile at all
+  // chunk: tiles a CTA; first: the first tile of the unit's sequence
+  __device__ __forceinline__ Parts(int chunk_, int first, int unit, int ntiles) {
+    chunk = max(chunk_, 1);
+    empty = ntiles == 0;
+    t0 = first + unit * ntiles;
     c0 = t0 / chunk;
     c1 = (t0 + ntiles - 1) / chunk;
   }
@@ -694,96 +861,144 @@ __device__ __forceinline__ float2 join_ml(const Args& a, const Parts& p, int row
   return make_float2(top, sum);
 }
 
-// Blocks below `rows`: one row each, whose parts the warps share.  Further
-// blocks: kWeightSlots slots of a pair each, weight_t += sum_r 2^(z_rt - lse_r),
-// the rows in their order.
+// The parts c0 + first, c0 + first + step, .. of a row, brought to the maximum
+// `base`: four dims a lane.
 template <int RPB>
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, int ctas, int64_t rows) {
+__device__ __forceinline__ float4 join_parts(const Args& a, const Parts& p, int row, float base, int first, int step) {
+  const int lane = threadIdx.x & 31;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = p.c0 + first; c <= p.c1; c += step) {
+    const int64_t at = static_cast<int64_t>(p.part(c)) * RPB + row;
+    const float f = ex2(a.part_ml[at].x - base);
+    const float4 y = reinterpret_cast<const float4*>(a.part_o + at * kKv4Dim)[lane];
+    o.x = fmaf(f, y.x, o.x);
+    o.y = fmaf(f, y.y, o.y);
+    o.z = fmaf(f, y.z, o.z);
+    o.w = fmaf(f, y.w, o.w);
+  }
+  return o;
+}
+
+// Blocks below `row_blocks` join `rpb` rows each: a warp a row, or, where a row
+// was cut into more than kWarpParts parts, all warps one after another.
+// Further blocks: kWeightSlots slots of a pair each,
+// weight_t += sum_r 2^(z_rt - lse_r), the rows in their order.
+constexpr int kWarpParts = 8;
+
+template <int RPB>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, int ctas, int rpb, int64_t rows,
+                                                                int64_t row_blocks) {
   __shared__ __align__(16) float so[kJoinWarps][kKv4Dim];
-  __shared__ float slse[64];
+  __shared__ float slse[kJoinWarps];
+  __shared__ int shared_row[kJoinWarps];   // this warp's row is for all
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
   const int64_t x = blockIdx.x;
-  if (x < rows) {
-    const int64_t bh = x / a.R;
-    const int r = static_cast<int>(x - bh * a.R);
-    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
-    const int row = r % RPB;
-    const int ntiles = tiles_of(kv4_length(a.lengths[b], a.cap, nullptr));
-    if (ntiles == 0) {
-      if (warp == 0) finish_row(a, b, h, r, lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, NEG_INF);
-      return;
+  const int chunk = tiles_per_cta(total_tiles(a, false), ctas);
+  if (x < row_blocks) {
+    const auto parts_of = [&](int64_t i, int* b, int* h, int* r) {   // of row i; ntiles 0: it sees no slot
+      const int64_t bh = i / a.R;
+      *r = static_cast<int>(i - bh * a.R);
+      *b = static_cast<int>(bh / a.H);
+      *h = static_cast<int>(bh - static_cast<int64_t>(*b) * a.H);
+      const int ntiles = tiles_of(kv4_length(a.lengths[*b], a.cap, nullptr));
+      return Parts(chunk, first_tile(a, *b), *h * a.RB + *r / RPB, ntiles);
+    };
+    const auto all_warps = [&](const Parts& p, int b, int h, int r) {
+      const float2 ml = join_ml<RPB>(a, p, r % RPB);
+      reinterpret_cast<float4*>(so[warp])[lane] =
+          join_parts<RPB>(a, p, r % RPB, ml.x == NEG_INF ? 0.f : ml.x, warp, kJoinWarps);
+      __syncthreads();
+      if (warp == 0) {
+        float4 o = reinterpret_cast<const float4*>(so[0])[lane];
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) {
+          const float4 y = reinterpret_cast<const float4*>(so[w])[lane];
+          o.x += y.x;
+          o.y += y.y;
+          o.z += y.z;
+          o.w += y.w;
+        }
+        finish_row(a, b, h, r, lane, o, ml.y, ml.x);
+      }
+    };
+    const int64_t i0 = x * rpb, mine = rpb == 1 ? i0 : i0 + warp;
+    int b, h, r;
+    if (lane == 0) shared_row[warp] = 0;
+    if (mine < rows) {
+      const Parts p = parts_of(mine, &b, &h, &r);
+      const int n = p.c1 - p.c0 + 1;
+      if (p.empty) {
+        if (rpb > 1 || warp == 0) finish_row(a, b, h, r, lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, NEG_INF);
+      } else if (rpb == 1) {
+        if (n > 1) all_warps(p, b, h, r);
+      } else if (n > kWarpParts) {
+        if (lane == 0) shared_row[warp] = 1;
+      } else if (n > 1) {
+        const float2 ml = join_ml<RPB>(a, p, r % RPB);
+        finish_row(a, b, h, r, lane, join_parts<RPB>(a, p, r % RPB, ml.x == NEG_INF ? 0.f : ml.x, 0, 1), ml.y, ml.x);
+      }
     }
-    Parts p;
-    p.find(a, ctas, b, h * a.RB + r / RPB, ntiles);
-    if (p.c0 == p.c1) return;
-    const float2 ml = join_ml<RPB>(a, p, row);
-    const float base = ml.x == NEG_INF ? 0.f : ml.x;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = p.c0 + warp; c <= p.c1; c += kJoinWarps) {
-      const int64_t at = static_cast<int64_t>(p.part(c)) * RPB + row;
-      const float f = ex2(a.part_ml[at].x - base);
-      const float4 y = reinterpret_cast<const float4*>(a.part_o + at * kKv4Dim)[lane];
-      o.x = fmaf(f, y.x, o.x);
-      o.y = fmaf(f, y.y, o.y);
-      o.z = fmaf(f, y.z, o.z);
-      o.w = fmaf(f, y.w, o.w);
-    }
-    reinterpret_cast<float4*>(so[warp])[lane] = o;
+    if (rpb == 1) return;
     __syncthreads();
-    if (warp) return;
-    const int n = min(kJoinWarps, p.c1 - p.c0 + 1);
-    for (int w = 1; w < n; ++w) {
-      const float4 y = reinterpret_cast<const float4*>(so[w])[lane];
-      o.x += y.x;
-      o.y += y.y;
-      o.z += y.z;
-      o.w += y.w;
+    for (int v = 0; v < rpb; ++v) {
+      if (!shared_row[v]) continue;
+      const Parts p = parts_of(i0 + v, &b, &h, &r);
+      all_warps(p, b, h, r);
+      __syncthreads();
     }
-    finish_row(a, b, h, r, lane, o, ml.y, ml.x);
     return;
   }
-  const int64_t per = (a.cap + kWeightSlots - 1) / kWeightSlots, y = x - rows;
+  const int64_t per = (a.cap + kWeightSlots - 1) / kWeightSlots, y = x - row_blocks;
   const int64_t bh = y / per;
-  const int64_t slot = (y - bh * per) * kWeightSlots + threadIdx.x * 4;
+  const int64_t slot0 = (y - bh * per) * kWeightSlots + threadIdx.x * 4;   // and kWeightSlots / 2 further on
   const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
   const int len = kv4_length(a.lengths[b], a.cap, nullptr);
   if ((y - bh * per) * kWeightSlots >= len) return;
   const int ntiles = tiles_of(len);
-  float4* w = reinterpret_cast<float4*>(a.weight + bh * a.cap + slot);   // capacities are multiples of 32
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int r0 = 0; r0 < a.R; r0 += 64) {
-    for (int r = r0 + warp; r < min(a.R, r0 + 64); r += kJoinWarps) {
-      Parts p;
-      p.find(a, ctas, b, h * a.RB + r / RPB, ntiles);
+  const int first = first_tile(a, b);
+  float4 sum[2] = {};
+  for (int r0 = 0; r0 < a.R; r0 += kJoinWarps) {
+    const int r = r0 + warp;   // each warp finds one row's log-sum
+    if (r < a.R) {
+      const Parts p(chunk, first, h * a.RB + r / RPB, ntiles);
       const float2 ml = p.c0 == p.c1 ? a.row_ml[bh * a.R + r] : join_ml<RPB>(a, p, r % RPB);
-      if (lane == 0) slse[r - r0] = row_log2(ml.y, ml.x);
+      if (lane == 0) slse[warp] = row_log2(ml.y, ml.x);
     }
     __syncthreads();
-    if (slot < len) {
-#pragma unroll 4
-      for (int r = r0; r < min(a.R, r0 + 64); ++r) {
-        const float lse = slse[r - r0];
-        const float4 z = *reinterpret_cast<const float4*>(a.logits + (bh * a.R + r) * a.cap + slot);
-        if (lse == NEG_INF) continue;
-        sum.x += ex2(z.x - lse);
-        sum.y += ex2(z.y - lse);
-        sum.z += ex2(z.z - lse);
-        sum.w += ex2(z.w - lse);
+#pragma unroll 2
+    for (int i = 0; i < min(kJoinWarps, a.R - r0); ++i) {
+      const float lse = slse[i];
+      const float* z = a.logits + (bh * a.R + r0 + i) * a.cap + slot0;
+      float4 v[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (slot0 + k * (kWeightSlots / 2) < len) v[k] = *reinterpret_cast<const float4*>(z + k * (kWeightSlots / 2));
+      if (lse == NEG_INF) continue;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        sum[k].x += ex2(v[k].x - lse);
+        sum[k].y += ex2(v[k].y - lse);
+        sum[k].z += ex2(v[k].z - lse);
+        sum[k].w += ex2(v[k].w - lse);
       }
     }
     __syncthreads();
   }
-  if (slot + 3 < len) {
-    const float4 v = *w;
-    *w = make_float4(v.x + sum.x, v.y + sum.y, v.z + sum.z, v.w + sum.w);
-  } else if (slot < len) {   // the slots behind the length keep what they hold
-    float* f = reinterpret_cast<float*>(w);
-    f[0] += sum.x;
-    if (slot + 1 < len) f[1] += sum.y;
-    if (slot + 2 < len) f[2] += sum.z;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t slot = slot0 + k * (kWeightSlots / 2);
+    float* f = a.weight + bh * a.cap + slot;   // (16-byte aligned: capacities are multiples of 32)
+    if (slot + 3 < len) {
+      const float4 v = *reinterpret_cast<float4*>(f);
+      *reinterpret_cast<float4*>(f) = make_float4(v.x + sum[k].x, v.y + sum[k].y, v.z + sum[k].z, v.w + sum[k].w);
+    } else if (slot < len) {   // the slots behind the length keep what they hold
+      f[0] += sum[k].x;
+      if (slot + 1 < len) f[1] += sum[k].y;
+      if (slot + 2 < len) f[2] += sum[k].z;
+    }
   }
 }
 
@@ -791,24 +1006,31 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
 int rows_of_block(int64_t R) { return R <= 8 ? 8 : 16; }
 
-template <int NT, bool kWeights>
+template <int NT, int kR, bool kWeights>
 cudaError_t launch_main(const Args& a, int* ctas, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0, sms = 1;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
-  const int64_t most = smem_bytes(8 * NT, 8 * NT);
   e = once.run(dev, [&] {
-    return cudaFuncSetAttribute(kv4_attn_kernel<NT, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(most));
+    return cudaFuncSetAttribute(kv4_attn_kernel<NT, kR, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(smem_bytes(8 * NT, 8 * NT, kR)));
   });
   if (e != cudaSuccess) return e;
-  const int64_t bytes = smem_bytes(a.R, 8 * NT);
+  const int64_t bytes = smem_bytes(a.R, 8 * NT, kR);
   // as many CTAs as an SM holds: registers allow 3 (2 with 16 rows), shared memory (1 KB a CTA is the system's) may
   // allow fewer
   const int64_t fit = 228 * 1024 / (bytes + 1024 + 256);
   *ctas = std::min(sms, kSmsMax) * static_cast<int>(std::min<int64_t>(NT == 1 ? 3 : 2, fit));
-  return launch_after(kv4_attn_kernel<NT, kWeights>, dim3(*ctas), kThreads, bytes, 1, stream, a);
+  return launch_after(kv4_attn_kernel<NT, kR, kWeights>, dim3(*ctas), kThreads, bytes, 1, stream, a);
+}
+
+template <bool kWeights>
+cudaError_t launch_rows(const Args& a, int* ctas, cudaStream_t stream) {
+  if (a.R == 1) return launch_main<1, 1, kWeights>(a, ctas, stream);
+  if (a.R == 2) return launch_main<1, 2, kWeights>(a, ctas, stream);
+  if (a.R <= 8) return launch_main<1, 0, kWeights>(a, ctas, stream);
+  return launch_main<2, 0, kWeights>(a, ctas, stream);
 }
 
 }  // namespace
@@ -854,18 +1076,19 @@ cudaError_t launch_kv4_attn(const Kv4AttnLaunch& p, cudaStream_t stream) {
   a.err = p.err;
   int ctas = 0;
   cudaError_t e;
-  if (rpb == 8)
-    e = p.weight ? launch_main<1, true>(a, &ctas, stream) : launch_main<1, false>(a, &ctas, stream);
-  else
-    e = p.weight ? launch_main<2, true>(a, &ctas, stream) : launch_main<2, false>(a, &ctas, stream);
+  e = p.weight ? launch_rows<true>(a, &ctas, stream) : launch_rows<false>(a, &ctas, stream);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.B) * p.H * R;
   const int64_t weight_blocks =
       p.weight ? static_cast<int64_t>(p.B) * p.H * ((p.cap + kWeightSlots - 1) / kWeightSlots) : 0;
-  if (rows + weight_blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(rows + weight_blocks));
-  return rpb == 8 ? launch_after(kv4_join_kernel<8>, grid, kJoinThreads, 0, 1, stream, a, ctas, rows)
-                  : launch_after(kv4_join_kernel<16>, grid, kJoinThreads, 0, 1, stream, a, ctas, rows);
+  // a warp a row where there are more rows than blocks fit the GPU at once (1,344 rows of a ragged batch: 8 us with a
+  // block each, 5 with a warp); fewer rows were cut into more parts each
+  const int per_block = rows > 4 * 148 ? kJoinWarps : 1;
+  const int64_t row_blocks = (rows + per_block - 1) / per_block;
+  if (row_blocks + weight_blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_after(rpb == 8 ? kv4_join_kernel<8> : kv4_join_kernel<16>,
+                      dim3(static_cast<unsigned>(row_blocks + weight_blocks)), kJoinThreads, 0, 1, stream, a, ctas,
+                      per_block, rows, row_blocks);
 }
 
 }  // namespace ulysses

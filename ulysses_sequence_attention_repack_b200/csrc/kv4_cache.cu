@@ -42,7 +42,7 @@ struct RowPlace {
 // sequences), then counts the ends that rows i0 + 1 .. pass.  cu is read inside
 // [0, batch] only, whatever it holds.
 template <int T>
-__device__ __forceinline__ RowPlace place_rows(const Kv4Rows& r, int64_t i0, int batch, int64_t capacity,
+__device__ __forceinline__ RowPlace place_rows(const Kv4Rows& r, int rows, int i0, int batch, int64_t capacity,
                                                unsigned int* err) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = batch;
@@ -55,23 +55,23 @@ __device__ __forceinline__ RowPlace place_rows(const Kv4Rows& r, int64_t i0, int
   const int b0 = lo + __popc(__ballot_sync(0xffffffffu, lo + lane <= hi && r.cu[min(lo + lane, hi)] <= i0)) - 1;
   int b = b0;
   if (T > 1) {
-    const int64_t end = b0 + 1 + lane <= batch ? r.cu[b0 + 1 + lane] : INT64_MAX;
+    const int end = b0 + 1 + lane <= batch ? r.cu[b0 + 1 + lane] : 0x7fffffff;
 #pragma unroll
     for (int u = 1; u < T; ++u) {
       const int n = __popc(__ballot_sync(0xffffffffu, end <= i0 + u));
       if (lane == u) b = b0 + n;
     }
   }
-  const int64_t i = i0 + lane;
+  const int i = i0 + lane;
   RowPlace p{0, -1};
-  if (lane >= T || i >= r.rows || b < 0 || b >= batch) return p;
+  if (lane >= T || i >= rows || b < 0 || b >= batch) return p;
   if (b == b0 + 32)   // many empty sequences in a row: go on one by one
     while (b < batch && r.cu[b + 1] <= i) ++b;
   if (b >= batch) return p;
-  const int64_t first = r.cu[b];
+  const int first = r.cu[b];
   if (i < first || i >= r.cu[b + 1]) return p;   // (sums that fall)
   p.b = b;
-  p.slot = static_cast<int64_t>(r.start[b]) + (i - first);
+  p.slot = static_cast<int64_t>(r.start[b]) + i - first;
   if (p.slot < 0 || p.slot >= capacity) {
     if (err) atomicOr(err, kErrCacheIndex);
     p.slot = -1;
@@ -96,8 +96,8 @@ __device__ __forceinline__ int meta_row(int at) {
   return kKv4MetaOffset + at * 16 + (at >> 5) * (kKv4BlockBytes - 32 * 16);
 }
 
-__device__ __forceinline__ int64_t row_offset(const Kv4Rows& r, int64_t i, int h) {
-  const int rank = h / r.heads_per_rank;
+__device__ __forceinline__ int64_t row_offset(const Kv4Rows& r, int64_t i, int h, int H) {
+  const int rank = r.heads_per_rank < H ? h / r.heads_per_rank : 0;
   return i * r.token_stride + rank * r.rank_stride + (h - rank * r.heads_per_rank) * r.head_stride;
 }
 
@@ -143,12 +143,10 @@ __device__ __noinline__ uint2 codes_by_division(uint4 w0, uint4 w1, float lo, fl
 // The codes of this lane's 16 values of a group, whose other values the lanes
 // of its quad hold; *meta gets the group's step and minimum.
 //
-// n = round((x - m) / s) without a division: t = d r rounded to an integer by
-// adding 1.5 2^23 (r an approximate 1 / s) is the right integer or, next to a
-// border, its neighbour.  The residual d - n s is exact (|d - n s| <= s is a
-// multiple of d's last place and of s's), so comparing it with s / 2 tells
-// which, and finds the ties, which go to even.  About one value in 300 of
-// bf16 data is such a tie; they are put right one after another.
+// n = round(d / s) of d = x - m by a quotient from an approximate reciprocal r
+// and one correction by its exact residual, which is the division's result;
+// above all it is exact where the quotient is half way between two codes (one
+// value in some 300 of bf16 data), so that adding 1.5 2^23 rounds those to even.
 __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* meta) {
   uint32_t lo2 = w[0], hi2 = w[0];
 #pragma unroll
@@ -162,20 +160,18 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* meta
     hi2 = max2(hi2, __shfl_xor_sync(0xffffffffu, hi2, d));
   }
   const float lo = min_nan(bf16_lo(lo2), bf16_hi(lo2)), hi = max_nan(bf16_lo(hi2), bf16_hi(hi2));
-  // (hi - lo) / 15 by its reciprocal and one correction, which is exact where the quotient is a bf16 border
+  // (hi - lo) / 15 in the same way; it is exact where the quotient is a bf16 border
   const float spread = __fsub_rn(hi, lo);
   const float q0 = spread * (1.0f / 15.0f);
   const float s = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-q0, 15.0f, spread), 1.0f / 15.0f, q0)));
-  const bool finite = fabsf(s) <= 3.4e38f && fabsf(lo) <= 3.4e38f;
-  *meta = finite ? (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u) : 0x7fc07fc0u;
+  const bool finite = spread <= 3.402823466e38f;   // then hi, lo and s are, too (false for NaN)
+  *meta = finite ? __byte_perm(__float_as_uint(s), __float_as_uint(lo), 0x7632u) : 0x7fc07fc0u;
   if (!(finite && s > 0.f)) return make_uint2(0, 0);
   if (s < 0x1p-100f)
     return codes_by_division(make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]), lo, s);
   constexpr float kRound = 12582912.f;   // 1.5 2^23, bits 0x4B400000
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  const float half = 0.5f * s;
-  uint32_t off = 0;   // bit e: value e lies half a step or more from its code
   uint32_t code[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -183,25 +179,9 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* meta
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float d = __fsub_rn(value_of(w, 8 * j + e), lo);
-      const float t = fmaf(d, r, kRound);
-      if (fabsf(fmaf(-(t - kRound), s, d)) >= half) off |= 1u << (8 * j + e);
-      code[j] += __float_as_uint(t) * (1u << (4 * e));
+      const float q = d * r;
+      code[j] += __float_as_uint(__fadd_rn(fmaf(fmaf(-q, s, d), r, q), kRound)) * (1u << (4 * e));
     }
-  }
-  while (off) {
-    const int e = __ffs(off) - 1, at = 4 * (e & 7);
-    off &= off - 1;
-    uint32_t u = 0, c = e < 8 ? code[0] : code[1];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u = (e >> 1) == i ? w[i] : u;
-    const uint32_t n = (c >> at) & 15u;
-    const float rest = fmaf(-static_cast<float>(n), s, __fsub_rn(e & 1 ? bf16_hi(u) : bf16_lo(u), lo));
-    // past the border, or on it and odd: one step towards the value
-    if (fabsf(rest) > half || (n & 1u)) c += rest > 0.f ? 1u << at : 0u - (1u << at);
-    if (e < 8)
-      code[0] = c;
-    else
-      code[1] = c;
   }
   return make_uint2(code[0], code[1]);
 }
@@ -216,27 +196,26 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], uint32_t* meta
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowsLaunch a) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t groups = (a.r.rows + kRun - 1) / kRun;
+  // (row numbers and items fit 32 bits: the launch sees to it)
+  const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5), group = item / a.H;
+  const int i0 = static_cast<int>(group) * kRun, h = static_cast<int>(item - group * a.H);
   pdl_wait();
-  if (item >= groups * a.H) return;
-  const int64_t i0 = item / a.H * kRun;
-  const int h = static_cast<int>(item - item / a.H * a.H);
+  if (item >= a.items) return;
   const int u = lane >> 2, q = lane & 3;   // token; which 8 of every 32 dims
-  const int64_t row = row_offset(a.r, i0 + u, h) + q * 8;
+  const int64_t row = row_offset(a.r, i0 + u, h, a.H) + q * 8;
   uint4 x[2][4];
 #pragma unroll
   for (int plane = 0; plane < 2; ++plane)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[plane][i] = make_uint4(0, 0, 0, 0);
-      if (i0 + u < a.r.rows) {
+      if (i0 + u < a.rows32) {
         const int4 v = ld_stream(reinterpret_cast<const int4*>(static_cast<const uint16_t*>(plane ? a.r.v : a.r.k) +
                                                                row + 32 * i));
         x[plane][i] = make_uint4(v.x, v.y, v.z, v.w);
       }
     }
-  const RowPlace mine = place_rows<kRun>(a.r, i0, a.B, a.cap, a.err);
+  const RowPlace mine = place_rows<kRun>(a.r, a.rows32, i0, a.B, a.cap, a.err);
   const int64_t slot = __shfl_sync(0xffffffffu, mine.slot, u);
   const int b = __shfl_sync(0xffffffffu, mine.b, u);
   const int64_t bh = static_cast<int64_t>(b) * a.H + h;
@@ -288,16 +267,14 @@ template <int T>
 __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const Kv4RowsLaunch a) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t groups = (a.r.rows + T - 1) / T;
+  const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5), group = item / a.H;
+  const int i0 = static_cast<int>(group) * T, h = static_cast<int>(item - group * a.H);
   pdl_wait();
-  if (item >= groups * a.H) return;
-  const int64_t i0 = item / a.H * T;
-  const int h = static_cast<int>(item - item / a.H * a.H);
+  if (item >= a.items) return;
   const int plane = lane >> 4, l16 = lane & 15;
   const int c_at = plane * kKv4VOffset + (l16 & 7) * 8 + (l16 >> 3) * 4, m_at = plane * 8 + (l16 >> 3) * 4;
-  uint16_t* dst = static_cast<uint16_t*>(plane ? a.r.v : a.r.k) + row_offset(a.r, i0, h) + l16 * 8;
-  const RowPlace mine = place_rows<T>(a.r, i0, a.B, a.cap, a.err);
+  uint16_t* dst = static_cast<uint16_t*>(plane ? a.r.v : a.r.k) + row_offset(a.r, i0, h, a.H) + l16 * 8;
+  const RowPlace mine = place_rows<T>(a.r, a.rows32, i0, a.B, a.cap, a.err);
   if (one_run<T>(mine)) {
     const int64_t slot0 = __shfl_sync(0xffffffffu, mine.slot, 0);
     const int64_t blk = kv4_block_offset(static_cast<int64_t>(__shfl_sync(0xffffffffu, mine.b, 0)) * a.H + h, a.cap,
@@ -598,14 +575,16 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4EvictLaun
 
 }  // namespace
 
-cudaError_t launch_kv4_rows(bool load, const Kv4RowsLaunch& a, cudaStream_t stream) {
+cudaError_t launch_kv4_rows(bool load, Kv4RowsLaunch a, cudaStream_t stream) {
   if (a.r.rows == 0) return cudaSuccess;
   // The load takes runs of tokens where sequences bring enough of them, and a
   // warp a token where they bring one or a few, which a run would take one by one.
   const bool runs = !load || a.r.rows >= static_cast<int64_t>(4 * kRun) * a.B;
   const int64_t items = runs ? (a.r.rows + kRun - 1) / kRun * a.H : a.r.rows * a.H;
   const int64_t grid = (items + kWarps - 1) / kWarps;
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  if (grid * kWarps > 0xffffffffll || grid > 0x7fffffff) return cudaErrorInvalidValue;
+  a.items = static_cast<uint32_t>(items);
+  a.rows32 = static_cast<int32_t>(a.r.rows);   // (at most 2^31 - 4096)
   const auto kernel = !load ? kv4_append_kernel : (runs ? kv4_load_kernel<kRun> : kv4_load_kernel<1>);
   return launch_after(kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, 1, stream, a);
 }
