@@ -432,6 +432,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       }
     }
 
+    // z^T = K q^T on the codes: d[row block][16-slot half][group].  Neighbouring
+    // products go to different sums, so none waits for the one before.
+    auto scores = [&](const uint8_t* blk, float (&d)[NT][2][2][4]) {
+      uint32_t wa[2][4], wb[2][4];   // the codes of slots g and g + 8
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint4 ka = *reinterpret_cast<const uint4*>(blk + (16 * mt + g) * 64 + t * 16);
+        const uint4 kb = *reinterpret_cast<const uint4*>(blk + (16 * mt + g + 8) * 64 + t * 16);
+        wa[mt][0] = ka.x;
+        wa[mt][1] = ka.y;
+        wa[mt][2] = ka.z;
+        wa[mt][3] = ka.w;
+        wb[mt][0] = kb.x;
+        wb[mt][1] = kb.y;
+        wb[mt][2] = kb.z;
+        wb[mt][3] = kb.w;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) (&d[nt][mt][0][0])[c] = 0.f;
+      }
+#pragma unroll
+      for (int v = 0; v < 4; v += 2)
+#pragma unroll
+        for (int up = 0; up < 2; ++up)   // nibbles 0, 1, 4, 5 of a word, then 2, 3, 6, 7
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t xa = wa[mt][v + w] >> (8 * up), xb = wb[mt][v + w] >> (8 * up);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma(d[nt][mt][w], xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[nt][4 * (v + w) + 2 * up],
+                    qf[nt][4 * (v + w) + 2 * up + 1]);
+            }
+    };
+
     // o^T += V^T p^T for the p s of a block
     uint32_t pb[2][NT][2][2];   // [group][row block][half][operand register]
     auto values = [&](const uint8_t* blk) {
@@ -486,28 +523,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
     // One block, a slot a lane.
     auto step_few = [&](auto edge_tag, const uint8_t* blk, int slot0) {
       constexpr bool kEdge = decltype(edge_tag)::value;
+      float d[NT][2][2][4];
+      scores(blk, d);
+      if (2 * t < kR) {   // the lanes with columns of rows
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const uint4 ka = *reinterpret_cast<const uint4*>(blk + (16 * mt + g) * 64 + t * 16);
-        const uint4 kb = *reinterpret_cast<const uint4*>(blk + (16 * mt + g + 8) * 64 + t * 16);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-        float d[2][4] = {};
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const uint32_t xa = wa[v] >> 8, xb = wb[v] >> 8;
-          mma(d[v & 1], wa[v] & kLow, wb[v] & kLow, wa[v] & kHigh, wb[v] & kHigh, qf[0][4 * v], qf[0][4 * v + 1]);
-          mma(d[v & 1], xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[0][4 * v + 2], qf[0][4 * v + 3]);
-        }
-        if (2 * t < kR) {   // the lanes with columns of rows
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint8_t* to = zbuf + (16 * mt + g + 8 * i) * (8 * kRows) + t * 16;
+            const float(&x)[2][4] = d[0][mt];
             if constexpr (kR == 1)
-              *reinterpret_cast<float2*>(to) = make_float2(d[0][2 * i], d[1][2 * i]);
+              *reinterpret_cast<float2*>(to) = make_float2(x[0][2 * i], x[1][2 * i]);
             else
-              *reinterpret_cast<float4*>(to) = make_float4(d[0][2 * i], d[1][2 * i], d[0][2 * i + 1], d[1][2 * i + 1]);
+              *reinterpret_cast<float4*>(to) = make_float4(x[0][2 * i], x[1][2 * i], x[0][2 * i + 1], x[1][2 * i + 1]);
           }
-        }
       }
       __syncwarp();
       const int slot = slot0 + lane;
@@ -601,26 +630,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       }
       __syncwarp();
       float s[NT][2][4];   // z / qscale: [16-slot half][slot g row 2t, g 2t+1, g+8 2t, g+8 2t+1]
+      float d[NT][2][2][4];
+      scores(blk, d);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const uint4 ka = *reinterpret_cast<const uint4*>(blk + (16 * mt + g) * 64 + t * 16);
-        const uint4 kb = *reinterpret_cast<const uint4*>(blk + (16 * mt + g + 8) * 64 + t * 16);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-        float d[NT][2][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) d[nt][0][c] = d[nt][1][c] = 0.f;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const uint32_t xa = wa[v] >> 8, xb = wb[v] >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma(d[nt][v & 1], wa[v] & kLow, wb[v] & kLow, wa[v] & kHigh, wb[v] & kHigh, qf[nt][4 * v],
-                qf[nt][4 * v + 1]);
-            mma(d[nt][v & 1], xa & kLow, xb & kLow, xa & kHigh, xb & kHigh, qf[nt][4 * v + 2], qf[nt][4 * v + 3]);
-          }
-        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float4 k = kput[16 * mt + g + 8 * i];
@@ -630,9 +643,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
 #pragma unroll
             for (int row = 0; row < 2; ++row) {
               const int c = 2 * i + row;
-              float x = k.x * d[nt][0][c];
+              float x = k.x * d[nt][mt][0][c];
               x = fmaf(k.y, qsum[nt][row][0], x);
-              x = fmaf(k.z, d[nt][1][c], x);
+              x = fmaf(k.z, d[nt][mt][1][c], x);
               x = fmaf(k.w, qsum[nt][row][1], x);
               if (kEdge && slot >= limit[nt][row]) x = NEG_INF;
               s[nt][mt][c] = x;
