@@ -25,8 +25,10 @@
 //
 // Roundings: q, codes, scales and minima enter exactly (q by a power of two,
 // which keeps its 8 bits down to 2^-28 of the row's largest); z, p, maxima and
-// sums are fp32; p s is rounded to fp16 for the second product (2^-11, for
-// twice the precision that bf16 would keep); o is rounded once, to bf16.
+// sums are fp32; p s is rounded to fp16 for the second product, off by at most
+// 2^-11 of itself (bf16's 2^-8 would show in o) and, since the largest sits at
+// 2^5 or more, by 2^-30 of the largest step for the smallest p; o is rounded
+// once, to bf16.
 //
 // Work split: the tiles of 128 slots of all (sequence, K/V head, block of
 // query rows) are one list, cut into equal runs, one a CTA, so ragged lengths
@@ -35,6 +37,15 @@
 // unfinished sum with its maximum in the workspace, and a second kernel joins
 // them.  The lists are found from the lengths on the device, so that a
 // captured launch stays right when they change.
+//
+// Measured (one B200, device time): 104,448 slots x 56 heads, one query row,
+// 842 MB: 140 us (6.0 TB/s of 6.55 measured) at 1.95 GHz, 158 us in a loop of
+// half a second, where the 1000 W cap holds 1.76 GHz; its copies alone take 125.
+// Memory and the ALU share the time: of 382 instructions a warp spends on a
+// block, 176 are the ANDs, shifts and byte moves that make operands of codes,
+// and the ALU runs at half rate.  With 8 rows 500 instructions a block bound it
+// (8 heads x 313,344 slots: 80 us, 4.5 TB/s), with 16 rows the dependences of
+// two warps a scheduler (14 heads x 104,448: 72 us, 2.9 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
