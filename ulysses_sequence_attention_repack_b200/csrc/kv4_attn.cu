@@ -183,9 +183,10 @@ struct Place {
         tile -= __shfl_sync(0xffffffffu, upto, 31);
       }
     }
-    ntiles = tiles_of(len);
-    unit = tile / ntiles;
-    lo = tile - unit * ntiles;
+    // (the bounds hold even if the lengths were changed meanwhile)
+    ntiles = max(tiles_of(len), 1);
+    unit = min(tile / ntiles, per - 1);
+    lo = min(tile - unit * ntiles, ntiles - 1);
   }
 
   // The first tile of the next unit; there is one.
@@ -193,10 +194,9 @@ struct Place {
     lo = 0;
     if (++unit < a.H * a.RB) return;
     unit = 0;
-    do {
-      len = ++b < a.B ? kv4_length(a.lengths[b], a.cap, nullptr) : 1;
-    } while (len == 0);
-    ntiles = tiles_of(len);
+    len = 0;
+    while (len == 0 && b < a.B - 1) len = kv4_length(a.lengths[++b], a.cap, nullptr);
+    ntiles = max(tiles_of(len), 1);
   }
 };
 
@@ -852,13 +852,14 @@ constexpr int kWeightSlots = kJoinThreads * 8;   // slots of a block that adds w
 struct Parts {
   int c0, c1, chunk, t0;
   bool empty;   // no tile at all
-  // chunk: tiles a CTA; first: the first tile of the unit's sequence
-  __device__ __forceinline__ Parts(int chunk_, int first, int unit, int ntiles) {
+  // chunk: tiles a CTA; first: the first tile of the unit's sequence.  (No CTA
+  // past the last, even if the lengths were changed meanwhile.)
+  __device__ __forceinline__ Parts(int chunk_, int ctas, int first, int unit, int ntiles) {
     chunk = max(chunk_, 1);
     empty = ntiles == 0;
     t0 = first + unit * ntiles;
-    c0 = t0 / chunk;
-    c1 = (t0 + ntiles - 1) / chunk;
+    c0 = min(t0 / chunk, ctas - 1);
+    c1 = min((t0 + ntiles - 1) / chunk, ctas - 1);
   }
   // a CTA's run begins with this unit, or it is the run's last
   __device__ __forceinline__ int part(int c) const { return 2 * c + (c * chunk >= t0 ? 0 : 1); }
@@ -928,7 +929,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, in
       *b = static_cast<int>(bh / a.H);
       *h = static_cast<int>(bh - static_cast<int64_t>(*b) * a.H);
       const int ntiles = tiles_of(kv4_length(a.lengths[*b], a.cap, nullptr));
-      return Parts(chunk, first_tile(a, *b), *h * a.RB + *r / RPB, ntiles);
+      return Parts(chunk, ctas, first_tile(a, *b), *h * a.RB + *r / RPB, ntiles);
     };
     const auto all_warps = [&](const Parts& p, int b, int h, int r) {
       const float2 ml = join_ml<RPB>(a, p, r % RPB);
@@ -987,7 +988,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, in
   for (int r0 = 0; r0 < a.R; r0 += kJoinWarps) {
     const int r = r0 + warp;   // each warp finds one row's log-sum
     if (r < a.R) {
-      const Parts p(chunk, first, h * a.RB + r / RPB, ntiles);
+      const Parts p(chunk, ctas, first, h * a.RB + r / RPB, ntiles);
       const float2 ml = p.c0 == p.c1 ? a.row_ml[bh * a.R + r] : join_ml<RPB>(a, p, r % RPB);
       if (lane == 0) slse[warp] = row_log2(ml.y, ml.x);
     }
