@@ -585,7 +585,7 @@ int ulysses_kv4_load(const ulysses_kv4_t* kv, const void* cache, void* k, void* 
                      int64_t head_stride, int64_t rank_stride, int32_t heads_per_rank, const int32_t* dev_cu,
                      const int32_t* dev_start, void* stream);
 
-/* Workspace of ulysses_kv4_attn (0 for a shape it refuses): about 10 or 20 MB
+/* Workspace of ulysses_kv4_attn (0 for a shape it refuses): about 4 or 8 MB
  * of unfinished sums and, with ULYSSES_KV4_WEIGHTS,
  * 4 * batch * q_heads * q_len * capacity bytes of logits. */
 size_t ulysses_kv4_attn_workspace_bytes(const ulysses_kv4_t* kv, int32_t q_heads, int32_t q_len, uint32_t flags);
@@ -596,8 +596,9 @@ size_t ulysses_kv4_attn_workspace_bytes(const ulysses_kv4_t* kv, int32_t q_heads
  * b*q_len + i, head h at (b*q_len + i)*q_token_stride + h*q_head_stride; query
  * heads h*G .. h*G + G-1 share K/V head h (G = q_heads / heads).  lse: NULL, or
  * fp32 [batch, q_heads, q_len], the base-2 log-sum-exp of the scaled logits. A
- * row that sees no slot gives zeros and -infinity.  With ULYSSES_KV4_WEIGHTS,
- * weights[b, h, t] += the sum of slot t's softmax weights over the rows of head
+ * row that sees no slot gives zeros and -infinity; one that sees some, of a q
+ * row that holds an infinity, a NaN or a magnitude of 2^115 or more, gives NaN.
+ * With ULYSSES_KV4_WEIGHTS, weights[b, h, t] += the sum of slot t's softmax weights over the rows of head
  * h.  fp32 logits, softmax and sums; weights times scales in fp16 for the second
  * product.  Meant for few rows (1 to about 16 = G * q_len); more work, each
  * further 16 reading the cache again.  Errors: ARG, ALIGN, DIVISIBILITY

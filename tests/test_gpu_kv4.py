@@ -421,6 +421,46 @@ def test_attention_of_values_of_very_different_sizes(gpu):
     _check_attn(kv, _host(kv, cache), q, out, lse, [n], False)
 
 
+@pytest.mark.parametrize("kscale,vscale,qscale", [(1.0, 1e36, 1.0), (1e30, 1e-30, 1e-30), (1e-30, 3e36, 1e30),
+                                                  (1.0, 1e-36, 1.0), (1.0, 3e-37, 1.0), (1e36, 1.0, 1e-37)])
+def test_attention_over_the_range_of_bf16(gpu, kscale, vscale, qscale):
+    import torch
+    n = 180
+    g = torch.Generator(device=gpu)
+    g.manual_seed(17)
+    kv = U.ulysses_kv4_plan(1, 2, D, 192)
+    cache = torch.zeros(kv.cache_bytes, dtype=torch.uint8, device=gpu)
+    k = (torch.randn((n, 2, D), generator=g, device=gpu) * kscale).to(torch.bfloat16)
+    v = (torch.randn((n, 2, D), generator=g, device=gpu) * vscale).to(torch.bfloat16)
+    U.ulysses_kv4_append(kv, cache, k, v, _i32([0, n], gpu), _i32([0], gpu))
+    for heads in (2, 10):                                # one query row a K/V head, and five
+        q = (torch.randn((1, 1, heads, D), generator=g, device=gpu) * qscale).to(torch.bfloat16)
+        out, lse = torch.empty_like(q), torch.empty((1, heads, 1), device=gpu)
+        ws = torch.empty(kv.workspace_bytes(heads, 1), dtype=torch.uint8, device=gpu)
+        U.ulysses_kv4_attn(kv, cache, q, out, _i32([n], gpu), SCALE, lse=lse, workspace=ws)
+        _check_attn(kv, _host(kv, cache), q, out, lse, [n], False)
+
+
+def test_attention_of_queries_past_the_range(gpu):
+    """A query row that reaches 2^115 gives NaN, whatever the keys; the rows beside it keep their results."""
+    import torch
+    for heads in (2, 10):
+        kv, cache, _, _ = _make(gpu, [100], 2, 128, 23)
+        g = torch.Generator(device=gpu)
+        g.manual_seed(24)
+        q = torch.randn((1, 1, heads, D), generator=g, device=gpu).to(torch.bfloat16)
+        out, lse = torch.empty_like(q), torch.empty((1, heads, 1), device=gpu)
+        ws = torch.empty(kv.workspace_bytes(heads, 1), dtype=torch.uint8, device=gpu)
+        U.ulysses_kv4_attn(kv, cache, q, out, _i32([100], gpu), SCALE, lse=lse, workspace=ws)
+        want, want_lse = out.clone(), lse.clone()
+        q[0, 0, 1] = 0
+        q[0, 0, 1, 5] = -2.0 ** 115
+        U.ulysses_kv4_attn(kv, cache, q, out, _i32([100], gpu), SCALE, lse=lse, workspace=ws)
+        assert torch.isnan(out[0, 0, 1]).all() and torch.isnan(lse[0, 1]).all()
+        rest = [h for h in range(heads) if h != 1]
+        assert torch.equal(out[0, 0, rest], want[0, 0, rest]) and torch.equal(lse[0, rest], want_lse[0, rest])
+
+
 def test_attention_keeps_nan_where_it_is_seen_only(gpu):
     """A NaN value row reaches the rows that see it, in its group alone; a row masked from it is untouched.
     A NaN key makes the rows that see it NaN."""

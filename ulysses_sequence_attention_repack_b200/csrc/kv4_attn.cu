@@ -73,6 +73,7 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = kSmsMax * kCtasPerSm;   // sizes the workspace; the grid never passes it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;                     // log2 by which a maximum may be passed before it moves
+constexpr int kLeastExp = -120;                  // of the power of two c of the scales
 constexpr int kHeadroom = 5;                     // p s 2^(5 - c) <= 2^8 2^2 2^5: inside fp16
 
 struct Args {
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int k = static_cast<int>(top >> 23) - 127;
-      const int e = max(-100, min(100, 14 - k));
+      const int e = max(-100, min(126, 14 - k));
       const float up = pow2(e);
       float sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -402,8 +403,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
         sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 2);
         sum[w] *= 0x1p-24f;
       }
-      // a row with an infinity or a NaN has no softmax: its logits are NaN
-      const float qs = top >= 0x7f800000u ? __int_as_float(0x7fc00000) : a.scale_log2 * pow2(24 - e);
+      // a row with an infinity or a NaN has no softmax: its logits are NaN; so are those of a row that reaches 2^115,
+      // which the powers of two do not
+      const float qs = top >= (115u + 127u) << 23 ? __int_as_float(0x7fc00000) : a.scale_log2 * pow2(24 - e);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {   // to the lanes that hold this row's z: rows 2t and 2t + 1
         const int from = 4 * (2 * t + c);
@@ -428,8 +430,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
 
     float acc[NT][8][4];
     float M[NT][2], Ms[NT][2], l[NT][2], z0[NT][2][2];   // Ms: M, or 0 while M is -inf
-    int c_exp[2] = {-100, -100};
-    float s_limit[2] = {pow2(-98), pow2(-98)}, s_up[2] = {pow2(kHeadroom + 100), pow2(kHeadroom + 100)};
+    int c_exp[2] = {kLeastExp, kLeastExp};
+    float s_limit[2] = {pow2(kLeastExp + 2), pow2(kLeastExp + 2)};
+    float s_up[2] = {pow2(kHeadroom - kLeastExp), pow2(kHeadroom - kLeastExp)};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(vs[w]));   // (scales are not negative)
-        const int c_new = max(c_exp[w], max(-100, min(100, static_cast<int>(big >> 23) - 127)));
+        const int c_new = max(c_exp[w], max(kLeastExp, min(124, static_cast<int>(big >> 23) - 127)));
         down[w] = ex2(static_cast<float>(c_exp[w] - c_new));
         c_exp[w] = c_new;
         s_limit[w] = pow2(c_new + 2);
@@ -789,13 +792,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
         }
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          // codes 2^-24, p s 2^(5 - c); the odd nibbles carry a further 16
-          const float even = pow2(24 - kHeadroom) * pow2(c_exp[w]), odd = even * 0.0625f, zz = z0[nt][c][w];
+          // codes 2^-24, p s 2^(5 - c); the odd nibbles carry a further 16.  (In two factors: together they may pass
+          // the range of fp32 where the values do not.)
+          const float even = pow2(24 - kHeadroom), odd = even * 0.0625f, up = pow2(c_exp[w]), zz = z0[nt][c][w];
           float4* dst = reinterpret_cast<float4*>(mo + (warp * mrows + row) * kKv4Dim + 64 * w + 8 * g);
-          dst[0] = make_float4(fmaf(acc[nt][4 * w][c], even, zz), fmaf(acc[nt][4 * w][c + 2], odd, zz),
-                               fmaf(acc[nt][4 * w + 1][c], even, zz), fmaf(acc[nt][4 * w + 1][c + 2], odd, zz));
-          dst[1] = make_float4(fmaf(acc[nt][4 * w + 2][c], even, zz), fmaf(acc[nt][4 * w + 2][c + 2], odd, zz),
-                               fmaf(acc[nt][4 * w + 3][c], even, zz), fmaf(acc[nt][4 * w + 3][c + 2], odd, zz));
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            dst[i] = make_float4(fmaf(acc[nt][4 * w + 2 * i][c] * even, up, zz),
+                                 fmaf(acc[nt][4 * w + 2 * i][c + 2] * odd, up, zz),
+                                 fmaf(acc[nt][4 * w + 2 * i + 1][c] * even, up, zz),
+                                 fmaf(acc[nt][4 * w + 2 * i + 1][c + 2] * odd, up, zz));
         }
       }
     __syncthreads();
