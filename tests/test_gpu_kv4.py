@@ -918,3 +918,114 @@ def test_binding_checks_shapes(gpu):
     empty = k[:0]
     U.ulysses_kv4_append(kv, cache, empty, empty, _i32([0, 0], gpu), st)     # nothing to do
     U.ulysses_kv4_load(kv, cache, empty, empty, _i32([0, 0], gpu), st)
+
+
+# ------------------------------------------------------------------------------------------ rows on their own
+
+def row_bound(q, k, v, vs, scale, o, p):
+    """As `bound`, element by element, with what one slot can cost another taken from p s instead of s:
+
+    * a row's power of two for a group is that of the largest p s it has met (the maximum and its p of the time, which
+      later maxima scale down for both), or 2^-114, so an operand below fp16's normal numbers is off by at most
+      2^-25 2^-5 of that: 2^-30 max p s + 2^-144 a slot, times codes of at most 15;
+    * the logits' terms are those of their own group (|m| and 15 s are at most twice the group's largest magnitude);
+    * a maximum moves by 2^8 at least, each time with an exp2 (2^-22) in what was summed before: at most
+      (range of z in powers of two) / 8 + 1 times.
+    """
+    n = k.shape[0]
+    u = 2.0 ** -24
+    mag = np.abs(v) + 15 * np.repeat(vs, 64, axis=1)
+    top = np.repeat(np.abs(k).reshape(n, 2, 64).max(2), 64, axis=1)
+    zmax = np.max(scale * ((np.abs(k) + 2 * top) @ np.abs(q)))
+    rel = 2 * 260 * u * zmax + 2.0 ** -21 + (2 * zmax * 1.45 / 8 + 1) * 2.0 ** -22
+    w = (p[:, None] * 15 * np.repeat(vs, 64, axis=1)).sum(0) * 2.0 ** -11
+    tiny = n * 15 * (np.repeat((p[:, None] * vs).max(0), 64) * 2.0 ** -30 + 2.0 ** -144)
+    sums = 2 * u * n * (p[:, None] * mag).sum(0)
+    core = rel * (p[:, None] * mag).sum(0) + w + tiny + sums
+    return core + (np.abs(o) + core) * 2.0 ** -8, 2 * 260 * u * zmax / np.log(2.0) + 2.0 ** -20
+
+
+def _check_rows(kv, host, q, out, lse, lens, causal, scale=SCALE, weights=None, before=None):
+    """Every row against the slots it sees and nothing else: a group of V that is not finite makes that group of the
+    row NaN, a K or a query that is not makes the row, its log-sum and its share of the weights NaN, and a row that
+    sees nothing gives zeros, -infinity and no weight, whatever its query is."""
+    B, q_len, q_heads, _ = q.shape
+    G = q_heads // kv.heads
+    qq, oo, ls = _f64(q), _f64(out), lse.cpu().numpy().astype(np.float64)
+    for b in range(B):
+        for h in range(kv.heads):
+            n = lens[b]
+            k, _ = host.values(b, h, 0, n, 0)
+            v, vs = host.values(b, h, 0, n, 1)
+            total, slack = np.zeros(n), np.zeros(n)
+            for i in range(q_len):
+                m = max(0, n - q_len + i + 1) if causal else n
+                for j in range(h * G, (h + 1) * G):
+                    where = (b, i, j)
+                    got = oo[b, i, j]
+                    if m == 0:
+                        assert not got.any() and ls[b, j, i] == -np.inf, where
+                        continue
+                    if not (np.isfinite(qq[b, i, j]).all() and np.isfinite(k[:m]).all()):
+                        assert np.isnan(got).all() and np.isnan(ls[b, j, i]), where
+                        total[:m] = np.nan
+                        continue
+                    seen = np.where(np.isfinite(vs[:m]), vs[:m], 0.0)
+                    vv = np.where(np.isfinite(v[:m]), v[:m], 0.0)
+                    o, z, p = orc.attention(qq[b, i, j], k[:m], vv, scale)
+                    tol, dz = row_bound(qq[b, i, j], k[:m], vv, seen, scale, o, p)
+                    nan = np.repeat(~np.isfinite(vs[:m]).all(0), 64)
+                    assert np.array_equal(np.isnan(got), nan), where
+                    err = np.abs(got - o)[~nan]
+                    assert np.all(err <= tol[~nan]), (*where, float((err / tol[~nan]).max()))
+                    dz += 2.0 ** -23 * abs(z)
+                    assert abs(ls[b, j, i] - z) <= dz, (*where, ls[b, j, i], z)
+                    total[:m] += p
+                    slack[:m] += p * 2 * dz + 2.0 ** -126
+            if weights is None:
+                continue
+            old, new = before[b, h].astype(np.float64), weights[b, h].astype(np.float64)
+            assert np.array_equal(np.isnan(new[:n]), np.isnan(total)), (b, h)
+            ok = ~np.isnan(total)
+            room = slack + 2.0 ** -23 * (G * q_len + 1) * (total + np.abs(old[:n]) + np.abs(new[:n]))
+            assert np.all(np.abs(new[:n] - old[:n] - total)[ok] <= room[ok]), (b, h)
+            assert np.array_equal(weights[b, h][n:].view(np.int32), before[b, h][n:].view(np.int32))
+
+
+# query tokens and heads that make 1 to 2, 3 to 8, 9 to 16 and more rows of a K/V head
+SHAPES = [(1, 1), (2, 1), (3, 1), (2, 4), (3, 3), (2, 8), (20, 1)]
+
+
+def _attend(dev, kv, cache, q, lens, causal, weights=False, scale=SCALE):
+    import torch
+    host = _host(kv, cache)
+    B, q_len, q_heads, _ = q.shape
+    out = torch.full((B, q_len, q_heads, D), 5.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((B, q_heads, q_len), 5.0, device=dev)
+    ws = torch.full((kv.workspace_bytes(q_heads, q_len, weights),), 0xFF, dtype=torch.uint8, device=dev)
+    U.ulysses_kv4_attn(kv, cache, q, out, _i32(lens, dev), scale, lse=lse, causal=causal, weights=weights,
+                       workspace=ws)
+    assert U.ulysses_kv4_last_device_error(kv) == 0
+    _check_rows(kv, host, q, out, lse, lens, causal, scale, _host(kv, cache).weight if weights else None,
+                host.weight)
+
+
+def _queries(dev, B, q_len, heads, seed):
+    import torch
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    return torch.randn((B, q_len, heads, D), generator=g, device=dev).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("q_len,G", SHAPES)
+@pytest.mark.parametrize("n", [8, 33, 200, 1000])
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(gpu, q_len, G, n):
+    """The newest token's V holds an infinity in one group of one head (and another sequence's a NaN): the tokens
+    before it, which do not see it, keep their values in that group too."""
+    kv, cache, k, v = _make(gpu, [n, n], 2, 1024, 100 + n)
+    bad = v[[n - 1, 2 * n - 1]].clone()
+    bad[0, 0, 70] = float("inf")
+    bad[1, 1, 3] = float("nan")
+    U.ulysses_kv4_append(kv, cache, k[[n - 1, 2 * n - 1]].contiguous(), bad, _i32([0, 1, 2], gpu),
+                         _i32([n - 1, n - 1], gpu))
+    _attend(gpu, kv, cache, _queries(gpu, 2, q_len, 2 * G, 101), [n, n], True)

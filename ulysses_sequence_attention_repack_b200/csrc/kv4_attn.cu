@@ -521,11 +521,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
     }
 
     // The powers of two of the scales, replaced because a slot's (each lane one) outgrew them: *down what that makes of
-    // finished sums.
+    // finished sums.  A step that is no number takes no part: p s carries it to the rows that see the slot, and as the
+    // largest it would take the others' p s to zero.
     auto grow_scales = [&](const float (&vs)[2], float (&down)[2]) {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(vs[w]));   // (scales are not negative)
+        const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs[w], 0.f)));   // (none is negative)
         const int c_new = max(c_exp[w], max(kLeastExp, min(124, static_cast<int>(big >> 23) - 127)));
         down[w] = ex2(static_cast<float>(c_exp[w] - c_new));
         c_exp[w] = c_new;
