@@ -1029,3 +1029,25 @@ def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(gpu, q_len,
     U.ulysses_kv4_append(kv, cache, k[[n - 1, 2 * n - 1]].contiguous(), bad, _i32([0, 1, 2], gpu),
                          _i32([n - 1, n - 1], gpu))
     _attend(gpu, kv, cache, _queries(gpu, 2, q_len, 2 * G, 101), [n, n], True)
+
+
+@pytest.mark.parametrize("q_len,G", SHAPES)
+@pytest.mark.parametrize("kind", ["hidden", "light", "lighter", "none", "early"])
+@pytest.mark.parametrize("n", [20, 300])
+def test_a_large_step_rounds_nothing_else(gpu, q_len, G, kind, n):
+    """Slots whose V steps are 2^30 times the others' and more, which some rows do not see or give hardly any weight:
+    the other slots' share of a row keeps its precision."""
+    import torch
+    kv, cache, k, v = _make(gpu, [n], 2, 320, 110 + n)
+    k, v = k.clone(), v.clone()
+    q = _queries(gpu, 1, q_len, 2 * G, 111).abs()           # so that a negative key is a light slot
+    if kind == "early":                                      # the first blocks of a warp, before its maximum rises
+        k[:n // 2] = k[:n // 2] * 0.1 - 3
+        v[:n // 2, :, :64] *= 2.0 ** 30
+    else:
+        at = n - 1 if kind == "hidden" else n // 2
+        if kind != "hidden":
+            k[at] = {"light": -1.5, "lighter": -4.0, "none": -20.0}[kind]
+        v[at, :, :64] *= 2.0 ** 40
+    U.ulysses_kv4_append(kv, cache, k, v, _i32([0, n], gpu), _i32([0], gpu))
+    _attend(gpu, kv, cache, q, [n], True)

@@ -20,15 +20,18 @@
 //   of o^T = V^T p^T, so the running maximum and sums need no exchange, and p
 //   becomes an operand of the second product by one 8 x 8 transpose.
 // - The maximum in the exponent is replaced only when a row's grows by more
-//   than 2^8, and the power of two that keeps p s inside fp16 only when the
-//   scales grow 4-fold, so most steps neither exchange nor rescale anything.
+//   than 2^8, and the power of two that keeps a row's p s inside fp16 with it or
+//   when p s has grown by 2^10, so most steps neither exchange nor rescale
+//   anything.  Both are the row's own, from the slots that it sees: a step
+//   that is large in a slot with hardly any weight, or in one that the row does
+//   not see, costs its other slots nothing.
 //
 // Roundings: q, codes, scales and minima enter exactly (q by a power of two,
 // which keeps its 8 bits down to 2^-28 of the row's largest); z, p, maxima and
 // sums are fp32; p s is rounded to fp16 for the second product, off by at most
-// 2^-11 of itself (bf16's 2^-8 would show in o) and, since the largest sits at
-// 2^5 or more, by 2^-30 of the largest step for the smallest p; o is rounded
-// once, to bf16.
+// 2^-11 of itself (bf16's 2^-8 would show in o) and, since the row's largest p s
+// sits at 2^5 or more, by 2^-30 of that for the smallest; o is rounded once, to
+// bf16.
 //
 // Work split: the tiles of 128 slots of all (sequence, K/V head, block of
 // query rows) are one list, cut into equal runs, one a CTA, so ragged lengths
@@ -73,8 +76,11 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = kSmsMax * kCtasPerSm;   // sizes the workspace; the grid never passes it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;                     // log2 by which a maximum may be passed before it moves
-constexpr int kLeastExp = -120;                  // of the power of two c of the scales
-constexpr int kHeadroom = 5;                     // p s 2^(5 - c) <= 2^8 2^2 2^5: inside fp16
+// The second product's operand is p s 2^(5 - c), at most 2^15; c follows the row's largest p s.
+constexpr int kHeadroom = 5;
+constexpr int kGrowSteps = 10;                   // powers of two by which p s may outgrow 2^c before c moves
+constexpr int kLeastExp = -114, kMostExp = 124;  // of c: p <= 2^8 times 2^(5 - c) is finite; no step passes 2^125
+constexpr float kMost = 32768.f;
 
 struct Args {
   const uint8_t* cache;
@@ -121,7 +127,37 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Both halves at once, in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 x, x, y, z; "
+      "mov.b64 {%0, %1}, x;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+__device__ __forceinline__ int exponent(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }   // x >= 0
+
+// A row's factor u = 2^(5 - c) of a group's p s, after a block whose largest p s is y, for a maximum whose move makes f
+// of what was summed before (1: it did not move; 0: nothing counted before).  Returns what the finished sums of
+// p s 2^(5 - c) are to be multiplied by.
+__device__ __forceinline__ float move_power(float& u, float f, float y) {
+  const int c = kHeadroom - exponent(u), top = exponent(y);
+  int to = c;
+  if (f != 1.f || top >= c + kGrowSteps)
+    to = min(kMostExp, max(kLeastExp, max(f > 0.f ? c + exponent(f) : kLeastExp, top)));
+  u = pow2(kHeadroom - to);
+  return f * pow2(max(-126, min(126, c - to)));
+}
 
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 #define NEG_INF __int_as_float(0xff800000)
@@ -343,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
     uint32_t qf[NT][16];
     float qscale[NT][2], qsum[NT][2][2];
     int limit[NT][2];
-    int lowest = len;
+    int lowest = len, highest = 0;             // of the rows' limits
     float rq[kRows], rq0[kRows], rq1[kRows];   // kR: scale and group sums of every row, and its limit
     int rlimit[kRows];
 #pragma unroll
@@ -414,7 +450,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
         qsum[nt][c][1] = __shfl_sync(0xffffffffu, sum[1], from);
         const int rr = row0 + 8 * nt + 2 * t + c;
         limit[nt][c] = rr < a.R ? (a.causal ? max(0, len - a.Lq + rr / a.G + 1) : len) : 0;
-        if (rr < a.R) lowest = min(lowest, limit[nt][c]);
+        if (rr < a.R) {
+          lowest = min(lowest, limit[nt][c]);
+          highest = max(highest, limit[nt][c]);
+        }
       }
       if constexpr (kR > 0) {
 #pragma unroll
@@ -427,12 +466,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       }
     }
     lowest = __reduce_min_sync(0xffffffffu, lowest);
+    highest = __reduce_max_sync(0xffffffffu, highest);
 
     float acc[NT][8][4];
-    float M[NT][2], Ms[NT][2], l[NT][2], z0[NT][2][2];   // Ms: M, or 0 while M is -inf
-    int c_exp[2] = {kLeastExp, kLeastExp};
+    float M[NT][2], Ms[NT][2], l[NT][2];   // Ms: M, or 0 while M is -inf
+    float2 z0[NT][2], u[NT][2];            // of both groups: sums of p m, the rows' factors of p s
+    // a step that takes no row's p s past its bound, whatever p is: 2^(c + 2) of the least c
     float s_limit[2] = {pow2(kLeastExp + 2), pow2(kLeastExp + 2)};
-    float s_up[2] = {pow2(kHeadroom - kLeastExp), pow2(kHeadroom - kLeastExp)};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -442,7 +482,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         M[nt][c] = NEG_INF;
-        Ms[nt][c] = l[nt][c] = z0[nt][c][0] = z0[nt][c][1] = 0.f;
+        Ms[nt][c] = l[nt][c] = 0.f;
+        z0[nt][c] = make_float2(0.f, 0.f);
+        u[nt][c] = make_float2(pow2(kHeadroom - kLeastExp), pow2(kHeadroom - kLeastExp));
       }
     }
 
@@ -513,27 +555,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       }
     };
 
-    float rM[kRows], rMs[kRows], rl[kRows], rz[kRows][2];   // kR: the same of every row; sums over this lane's slots
+    // kR: the same of every row; sums over this lane's slots
+    float rM[kRows], rMs[kRows], rl[kRows], rz[kRows][2], ru[kRows][2];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       rM[r] = NEG_INF;
       rMs[r] = rl[r] = rz[r][0] = rz[r][1] = 0.f;
+      ru[r][0] = ru[r][1] = pow2(kHeadroom - kLeastExp);
     }
-
-    // The powers of two of the scales, replaced because a slot's (each lane one) outgrew them: *down what that makes of
-    // finished sums.  A step that is no number takes no part: p s carries it to the rows that see the slot, and as the
-    // largest it would take the others' p s to zero.
-    auto grow_scales = [&](const float (&vs)[2], float (&down)[2]) {
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs[w], 0.f)));   // (none is negative)
-        const int c_new = max(c_exp[w], max(kLeastExp, min(124, static_cast<int>(big >> 23) - 127)));
-        down[w] = ex2(static_cast<float>(c_exp[w] - c_new));
-        c_exp[w] = c_new;
-        s_limit[w] = pow2(c_new + 2);
-        s_up[w] = pow2(kHeadroom - c_new);
-      }
-    };
 
     // One block, a slot a lane.
     auto step_few = [&](auto edge_tag, const uint8_t* blk, int slot0) {
@@ -556,10 +585,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       __syncwarp();
       const int slot = slot0 + lane;
       uint4 m = *reinterpret_cast<const uint4*>(blk + kKv4MetaOffset + lane * 16);
-      if (kEdge && slot >= len) m = make_uint4(0, 0, 0, 0);   // anything may be held there
+      if (kEdge && slot >= highest) m = make_uint4(0, 0, 0, 0);   // no row sees it; anything may be held there
       const float vs[2] = {bf16_lo(m.z), bf16_lo(m.w)}, vm[2] = {bf16_hi(m.z), bf16_hi(m.w)};
-      float z[kRows];
-      bool move = vs[0] > s_limit[0] || vs[1] > s_limit[1];
+      float z[kRows] = {}, p[kRows], ps[kRows][2];
+      const auto weigh = [&](int r) {   // p, and p s as the operand
+        p[r] = ex2(z[r] - rMs[r]);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)   // (whatever the steps of an unseen slot are)
+          ps[r][w] = kEdge && slot >= rlimit[r] ? 0.f : p[r] * ru[r][w] * vs[w];
+      };
+      bool move = false;
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         const float2 d = *reinterpret_cast<const float2*>(zbuf + lane * (8 * kRows) + r * 8);
@@ -570,42 +605,46 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
         x *= rq[r];
         if (kEdge && slot >= rlimit[r]) x = NEG_INF;
         z[r] = x;
-        move |= x > rM[r] + kGrow;
+        weigh(r);
+        move |= x > rM[r] + kGrow || ps[r][0] > kMost || ps[r][1] > kMost;
         if (kWeights && r < a.R && (!kEdge || slot < len)) a.logits[(bh * a.R + r) * a.cap + slot] = x;
       }
       if (__any_sync(0xffffffffu, move)) {
-        float down[2];
-        grow_scales(vs, down);
-        float al[2] = {1.f, 1.f};   // of this lane's columns of o^T
+        float fac[2][2] = {{1.f, 1.f}, {1.f, 1.f}};   // of this lane's columns of o^T, in each group
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           float top = z[r];
 #pragma unroll
           for (int dlt = 16; dlt; dlt >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, dlt));
-          const float m_new = fmaxf(rM[r], top);
+          const float m_new = top > rM[r] + kGrow ? top : rM[r];
           const float f = m_new == rM[r] ? 1.f : ex2(rM[r] - m_new);
           rM[r] = m_new;
           rMs[r] = m_new == NEG_INF ? 0.f : m_new;
           rl[r] *= f;
           rz[r][0] *= f;
           rz[r][1] *= f;
-          if (t == (r >> 1)) al[r & 1] = f;
+          const float now = kEdge && slot >= rlimit[r] ? 0.f : ex2(z[r] - rMs[r]);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            // (what is no number takes no part: as the largest it would take the others' to zero)
+            const uint32_t y = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(now * vs[w], 0.f)));
+            const float down = move_power(ru[r][w], f, __uint_as_float(y));
+            if (t == (r >> 1)) fac[r & 1][w] = down;
+          }
+          weigh(r);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[0][i][c] *= al[c & 1] * down[i >> 2];
+          for (int c = 0; c < 4; ++c) acc[0][i][c] *= fac[c & 1][i >> 2];
       }
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        const float p = ex2(z[r] - rMs[r]);
-        rl[r] += p;
-        float w0 = p * (vs[0] * s_up[0]), w1 = p * (vs[1] * s_up[1]);
-        const bool unseen = kEdge && slot >= rlimit[r];   // (whatever this slot's scales are)
-        if (unseen) w0 = w1 = 0.f;
-        rz[r][0] = fmaf(p, unseen ? 0.f : vm[0], rz[r][0]);
-        rz[r][1] = fmaf(p, unseen ? 0.f : vm[1], rz[r][1]);
-        const uint32_t both = pack_f16(w0, w1);
+        rl[r] += p[r];
+        const bool unseen = kEdge && slot >= rlimit[r];
+        rz[r][0] = fmaf(p[r], unseen ? 0.f : vm[0], rz[r][0]);
+        rz[r][1] = fmaf(p[r], unseen ? 0.f : vm[1], rz[r][1]);
+        const uint32_t both = pack_f16(ps[r][0], ps[r][1]);
         *reinterpret_cast<uint16_t*>(wput + r * 128) = static_cast<uint16_t>(both);
         *reinterpret_cast<uint16_t*>(wput + r * 128 + 64) = static_cast<uint16_t>(both >> 16);
       }
@@ -625,23 +664,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
     auto step = [&](auto edge_tag, const uint8_t* blk, int slot0) {
       constexpr bool kEdge = decltype(edge_tag)::value;
       // each lane turns one slot's scales and minima into fp32 for all
+      bool big;   // a step that may take a p s past its bound
       {
         uint4 m = *reinterpret_cast<const uint4*>(blk + kKv4MetaOffset + lane * 16);
-        // slots behind the length hold anything: nothing of them may reach a sum
-        if (kEdge && slot0 + lane >= len) m = make_uint4(0, 0, 0, 0);
+        // slots that no row sees hold anything: nothing of them may reach a sum
+        if (kEdge && slot0 + lane >= highest) m = make_uint4(0, 0, 0, 0);
         const float vs[2] = {bf16_lo(m.z), bf16_lo(m.w)};
-        if (__any_sync(0xffffffffu, vs[0] > s_limit[0] || vs[1] > s_limit[1])) {
-          float down[2];
-          grow_scales(vs, down);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) acc[nt][i][c] *= down[i >> 2];
-        }
+        big = __any_sync(0xffffffffu, vs[0] > s_limit[0] || vs[1] > s_limit[1]);
         kput[lane] = make_float4(bf16_lo(m.x), bf16_hi(m.x), bf16_lo(m.y), bf16_hi(m.y));
-        kput[32 + lane] = make_float4(vs[0] * s_up[0], bf16_hi(m.z), vs[1] * s_up[1], bf16_hi(m.w));
+        kput[32 + lane] = make_float4(vs[0], vs[1], bf16_hi(m.z), bf16_hi(m.w));
       }
       __syncwarp();
       float s[NT][2][4];   // z / qscale: [16-slot half][slot g row 2t, g 2t+1, g+8 2t, g+8 2t+1]
@@ -680,7 +711,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
           top[nt][c] = fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2])) * qscale[nt][c];
           move |= top[nt][c] > M[nt][c] + kGrow;
         }
+      if (big) {   // by the rows' largest p in this block
+        const float4 mine = kput[32 + lane];
+        const float s0 = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mine.x, 0.f))));
+        const float s1 = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mine.y, 0.f))));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float p = ex2(top[nt][c] - Ms[nt][c]);
+            move |= p * u[nt][c].x * s0 > kMost || p * u[nt][c].y * s1 > kMost;
+          }
+      }
       if (__any_sync(0xffffffffu, move)) {
+        float up[2] = {pow2(kHeadroom - kMostExp), pow2(kHeadroom - kMostExp)};   // largest factor of a row with slots
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -689,19 +733,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float m_new = fmaxf(M[nt][c], m);
-            const float al = m_new == M[nt][c] ? 1.f : ex2(M[nt][c] - m_new);
+            const float m_new = m > M[nt][c] + kGrow ? m : M[nt][c];
+            const float f = m_new == M[nt][c] ? 1.f : ex2(M[nt][c] - m_new);
             M[nt][c] = m_new;
             Ms[nt][c] = m_new == NEG_INF ? 0.f : m_new;
-            l[nt][c] *= al;
-            z0[nt][c][0] *= al;
-            z0[nt][c][1] *= al;
+            l[nt][c] *= f;
+            z0[nt][c].x *= f;
+            z0[nt][c].y *= f;
+            float y[2] = {0.f, 0.f};   // the row's largest p s (what is no number takes no part)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 v = kput[32 + 8 * k + g];
+              float p = ex2(fmaf(s[nt][k >> 1][2 * (k & 1) + c], qscale[nt][c], -Ms[nt][c]));
+              if (kEdge && slot0 + 8 * k + g >= limit[nt][c]) p = 0.f;
+              y[0] = fmaxf(y[0], p * v.x);
+              y[1] = fmaxf(y[1], p * v.y);
+            }
+            // both groups' in one word: their leading halves, whose order is theirs
+            uint32_t both = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632u);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, d));
+            const float down0 = move_power(u[nt][c].x, f, bf16_lo(both)), down1 = move_power(u[nt][c].y, f, bf16_hi(both));
+            if (m_new != NEG_INF) {
+              up[0] = fmaxf(up[0], u[nt][c].x);
+              up[1] = fmaxf(up[1], u[nt][c].y);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              acc[nt][i][c] *= al;
-              acc[nt][i][c + 2] *= al;
+              acc[nt][i][c] *= i < 4 ? down0 : down1;
+              acc[nt][i][c + 2] *= i < 4 ? down0 : down1;
             }
           }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          up[w] = fmaxf(up[w], __shfl_xor_sync(0xffffffffu, up[w], 1));
+          up[w] = fmaxf(up[w], __shfl_xor_sync(0xffffffffu, up[w], 2));
+          s_limit[w] = pow2(kHeadroom + 2 - exponent(up[w]));
+        }
       }
       // p, its sums, and p s as the operand of the second product
 #pragma unroll
@@ -716,12 +784,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
             const float4& v = i ? vb : va;
             const float p = ex2(fmaf(s[nt][mt][c], qscale[nt][row], -Ms[nt][row]));
             l[nt][row] += p;
-            w0[c] = p * v.x;
-            w1[c] = p * v.z;
-            float m0 = v.y, m1 = v.w;
-            if (kEdge && slot0 + 16 * mt + g + 8 * i >= limit[nt][row]) w0[c] = w1[c] = m0 = m1 = 0.f;
-            z0[nt][row][0] = fmaf(p, m0, z0[nt][row][0]);
-            z0[nt][row][1] = fmaf(p, m1, z0[nt][row][1]);
+            // both groups in one (104,448 slots x 56 heads, 4 rows: 187 us one by one, 178 in pairs)
+            const float2 pp = make_float2(p, p);
+            float2 ps = mul2(mul2(pp, u[nt][row]), make_float2(v.x, v.y)), vm = make_float2(v.z, v.w);
+            if (kEdge && slot0 + 16 * mt + g + 8 * i >= limit[nt][row]) ps = vm = make_float2(0.f, 0.f);
+            w0[c] = ps.x;
+            w1[c] = ps.y;
+            z0[nt][row] = fma2(pp, vm, z0[nt][row]);
           }
           pb[0][nt][mt][0] = transpose8x8(pack_f16(w0[0], w0[1]));
           pb[0][nt][mt][1] = transpose8x8(pack_f16(w0[2], w0[3]));
@@ -770,8 +839,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
         if (t == (r >> 1)) {
           M[0][r & 1] = rM[r];
           l[0][r & 1] = rl[r];
-          z0[0][r & 1][0] = rz[r][0];
-          z0[0][r & 1][1] = rz[r][1];
+          z0[0][r & 1] = make_float2(rz[r][0], rz[r][1]);
+          u[0][r & 1] = make_float2(ru[r][0], ru[r][1]);
         }
       }
     }
@@ -782,8 +851,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
 #pragma unroll
         for (int dlt = 4; dlt < 32 && kR == 0; dlt <<= 1) {
           l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], dlt);
-          z0[nt][c][0] += __shfl_xor_sync(0xffffffffu, z0[nt][c][0], dlt);
-          z0[nt][c][1] += __shfl_xor_sync(0xffffffffu, z0[nt][c][1], dlt);
+          z0[nt][c].x += __shfl_xor_sync(0xffffffffu, z0[nt][c].x, dlt);
+          z0[nt][c].y += __shfl_xor_sync(0xffffffffu, z0[nt][c].y, dlt);
         }
         const int row = 8 * nt + 2 * t + c;
         if (row >= mrows) continue;
@@ -795,7 +864,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
         for (int w = 0; w < 2; ++w) {
           // codes 2^-24, p s 2^(5 - c); the odd nibbles carry a further 16.  (In two factors: together they may pass
           // the range of fp32 where the values do not.)
-          const float even = pow2(24 - kHeadroom), odd = even * 0.0625f, up = pow2(c_exp[w]), zz = z0[nt][c][w];
+          const float even = pow2(24 - kHeadroom), odd = even * 0.0625f, zz = w ? z0[nt][c].y : z0[nt][c].x;
+          const float up = pow2(kHeadroom - exponent(w ? u[nt][c].y : u[nt][c].x));
           float4* dst = reinterpret_cast<float4*>(mo + (warp * mrows + row) * kKv4Dim + 64 * w + 8 * g);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
