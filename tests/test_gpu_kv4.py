@@ -1051,3 +1051,27 @@ def test_a_large_step_rounds_nothing_else(gpu, q_len, G, kind, n):
         v[at, :, :64] *= 2.0 ** 40
     U.ulysses_kv4_append(kv, cache, k, v, _i32([0, n], gpu), _i32([0], gpu))
     _attend(gpu, kv, cache, q, [n], True)
+
+
+@pytest.mark.parametrize("q_len,G", SHAPES)
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("n", [1, 2, 19])
+def test_rows_that_see_nothing_give_zeros_whatever_their_query(gpu, q_len, G, weights, n):
+    """Fewer slots than queries: the first ones see none, and what is in them (padding, say) does not count."""
+    kv, cache, _, _ = _make(gpu, [n, n], 2, 32, 120)
+    q = _queries(gpu, 2, q_len, 2 * G, 121)
+    unseen = max(0, q_len - n)
+    q[0, :unseen, 0] = float("nan")
+    q[0, :unseen, -1, 7] = float("-inf")
+    q[1, :unseen, 0, 100] = 2.0 ** 120
+    _attend(gpu, kv, cache, q, [n, n], True, weights)
+
+
+@pytest.mark.parametrize("q_len,G", SHAPES)
+@pytest.mark.parametrize("weights", [False, True])
+def test_a_zero_query_at_a_very_small_scale(gpu, q_len, G, weights):
+    """All logits are 0 however small the scale: equal weights for the slots that are seen."""
+    kv, cache, _, _ = _make(gpu, [45], 2, 64, 122)
+    q = _queries(gpu, 1, q_len, 2 * G, 123)
+    q[:, ::2] = 0
+    _attend(gpu, kv, cache, q, [45], True, weights, scale=1e-30)

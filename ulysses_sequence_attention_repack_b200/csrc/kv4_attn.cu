@@ -697,7 +697,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
               s[nt][mt][c] = x;
               if (kWeights) {
                 const int r = row0 + 8 * nt + 2 * t + row;
-                if (r < a.R && (!kEdge || slot < len)) a.logits[(bh * a.R + r) * a.cap + slot] = x * qscale[nt][row];
+                const float z = kEdge && slot >= limit[nt][row] ? NEG_INF : x * qscale[nt][row];
+                if (r < a.R && (!kEdge || slot < len)) a.logits[(bh * a.R + r) * a.cap + slot] = z;
               }
             }
         }
@@ -782,12 +783,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
           for (int c = 0; c < 4; ++c) {
             const int i = c >> 1, row = c & 1;
             const float4& v = i ? vb : va;
-            const float p = ex2(fmaf(s[nt][mt][c], qscale[nt][row], -Ms[nt][row]));
+            float p = ex2(fmaf(s[nt][mt][c], qscale[nt][row], -Ms[nt][row]));
+            // (0 by the limit, not by s = -inf alone: the row's scale is NaN where its query is, and may be 0)
+            const bool unseen = kEdge && slot0 + 16 * mt + g + 8 * i >= limit[nt][row];
+            if (unseen) p = 0.f;
             l[nt][row] += p;
             // both groups in one (104,448 slots x 56 heads, 4 rows: 187 us one by one, 178 in pairs)
             const float2 pp = make_float2(p, p);
             float2 ps = mul2(mul2(pp, u[nt][row]), make_float2(v.x, v.y)), vm = make_float2(v.z, v.w);
-            if (kEdge && slot0 + 16 * mt + g + 8 * i >= limit[nt][row]) ps = vm = make_float2(0.f, 0.f);
+            if (unseen) ps = vm = make_float2(0.f, 0.f);   // (whatever the slot's steps are)
             w0[c] = ps.x;
             w1[c] = ps.y;
             z0[nt][row] = fma2(pp, vm, z0[nt][row]);
