@@ -1075,3 +1075,21 @@ def test_a_zero_query_at_a_very_small_scale(gpu, q_len, G, weights):
     q = _queries(gpu, 1, q_len, 2 * G, 123)
     q[:, ::2] = 0
     _attend(gpu, kv, cache, q, [45], True, weights, scale=1e-30)
+
+
+@pytest.mark.parametrize("q_len,G", SHAPES)
+@pytest.mark.parametrize("n", [24, 150])
+def test_a_row_without_a_softmax_adds_no_weight_to_slots_it_does_not_see(gpu, q_len, G, n):
+    """A query that is not finite makes the weights of the slots it sees NaN, and of no others; nor does a key that is
+    not finite reach the weights of rows before it."""
+    import torch
+    kv, cache, k, v = _make(gpu, [n, n], 2, 160, 130)
+    at = kv.weight_offset
+    w = torch.rand(2 * 2 * 160, device=gpu)
+    cache[at:at + 4 * w.numel()].view(torch.float32).copy_(w)
+    q = _queries(gpu, 2, q_len, 2 * G, 131)
+    q[0, 0, 0, 5] = float("nan")
+    bad = k[2 * n - 1:].clone()
+    bad[0, 1, 9] = float("inf")
+    U.ulysses_kv4_append(kv, cache, bad, v[2 * n - 1:].contiguous(), _i32([0, 0, 1], gpu), _i32([0, n - 1], gpu))
+    _attend(gpu, kv, cache, q, [n, n], True, True)

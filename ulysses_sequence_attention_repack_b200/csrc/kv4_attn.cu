@@ -159,6 +159,11 @@ __device__ __forceinline__ float move_power(float& u, float f, float y) {
   return f * pow2(max(-126, min(126, c - to)));
 }
 
+// Slots below this are seen by row r of a sequence of len slots.
+__device__ __forceinline__ int row_limit(const Args& a, int len, int r) {
+  return a.causal ? max(0, len - a.Lq + r / a.G + 1) : len;
+}
+
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 #define NEG_INF __int_as_float(0xff800000)
 
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
         qsum[nt][c][0] = __shfl_sync(0xffffffffu, sum[0], from);
         qsum[nt][c][1] = __shfl_sync(0xffffffffu, sum[1], from);
         const int rr = row0 + 8 * nt + 2 * t + c;
-        limit[nt][c] = rr < a.R ? (a.causal ? max(0, len - a.Lq + rr / a.G + 1) : len) : 0;
+        limit[nt][c] = rr < a.R ? row_limit(a, len, rr) : 0;
         if (rr < a.R) {
           lowest = min(lowest, limit[nt][c]);
           highest = max(highest, limit[nt][c]);
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
           rq[rr] = __shfl_sync(0xffffffffu, qs, 4 * rr);
           rq0[rr] = __shfl_sync(0xffffffffu, sum[0], 4 * rr);
           rq1[rr] = __shfl_sync(0xffffffffu, sum[1], 4 * rr);
-          rlimit[rr] = rr < a.R ? (a.causal ? max(0, len - a.Lq + rr / a.G + 1) : len) : 0;
+          rlimit[rr] = rr < a.R ? row_limit(a, len, rr) : 0;
         }
       }
     }
@@ -1117,6 +1122,18 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, in
       for (int k = 0; k < 2; ++k)
         if (slot0 + k * (kWeightSlots / 2) < len) v[k] = *reinterpret_cast<const float4*>(z + k * (kWeightSlots / 2));
       if (lse == NEG_INF) continue;
+      if (lse != lse) {   // a row without a softmax: no number for the slots it sees, nothing for the others
+        const int limit = row_limit(a, len, r0 + i);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int64_t slot = slot0 + k * (kWeightSlots / 2);
+          if (slot < limit) sum[k].x = lse;
+          if (slot + 1 < limit) sum[k].y = lse;
+          if (slot + 2 < limit) sum[k].z = lse;
+          if (slot + 3 < limit) sum[k].w = lse;
+        }
+        continue;
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         sum[k].x += ex2(v[k].x - lse);
