@@ -597,7 +597,8 @@ size_t ulysses_kv4_attn_workspace_bytes(const ulysses_kv4_t* kv, int32_t q_heads
  * heads h*G .. h*G + G-1 share K/V head h (G = q_heads / heads).  lse: NULL, or
  * fp32 [batch, q_heads, q_len], the base-2 log-sum-exp of the scaled logits. A
  * row that sees no slot gives zeros and -infinity; one that sees some, of a q
- * row that holds an infinity, a NaN or a magnitude of 2^115 or more, gives NaN.
+ * row that holds an infinity, a NaN or a magnitude of 2^115 or more, or whose
+ * logits leave the range of fp32 (one above it, or all below), gives NaN.
  * With ULYSSES_KV4_WEIGHTS, weights[b, h, t] += the sum of slot t's softmax weights over the rows of head
  * h.  fp32 logits, softmax and sums; weights times scales in fp16 for the second
  * product.  Meant for few rows (1 to about 16 = G * q_len); more work, each

@@ -1093,3 +1093,28 @@ def test_a_row_without_a_softmax_adds_no_weight_to_slots_it_does_not_see(gpu, q_
     bad[0, 1, 9] = float("inf")
     U.ulysses_kv4_append(kv, cache, bad, v[2 * n - 1:].contiguous(), _i32([0, 0, 1], gpu), _i32([0, n - 1], gpu))
     _attend(gpu, kv, cache, q, [n, n], True, True)
+
+
+@pytest.mark.parametrize("q_len,G", SHAPES)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_logits_past_the_range_of_fp32_give_nan(gpu, q_len, G, sign):
+    """Keys and queries of 1e30: no logit that is seen is a number, and the row says so instead of passing for one
+    that sees nothing.  The head beside it keeps its results."""
+    import torch
+    n = 70
+    kv, cache, k, v = _make(gpu, [n], 2, 96, 140)
+    q = _queries(gpu, 1, q_len, 2 * G, 141)
+    out, lse = torch.empty_like(q), torch.empty((1, 2 * G, q_len), device=gpu)
+    ws = torch.empty(kv.workspace_bytes(2 * G, q_len, True), dtype=torch.uint8, device=gpu)
+    U.ulysses_kv4_attn(kv, cache, q, out, _i32([n], gpu), SCALE, lse=lse, causal=True, workspace=ws)
+    want, want_lse = out.clone(), lse.clone()
+    k[:, 0] = k[:, 0].abs() * 1e30
+    q[:, :, :G] = q[:, :, :G].abs() * (sign * 1e30)
+    U.ulysses_kv4_append(kv, cache, k, v, _i32([0, n], gpu), _i32([0], gpu))
+    U.ulysses_kv4_attn(kv, cache, q, out, _i32([n], gpu), SCALE, lse=lse, causal=True, weights=True, workspace=ws)
+    assert torch.isnan(out[:, :, :G]).all() and torch.isnan(lse[:, :G]).all()
+    assert torch.equal(out[:, :, G:], want[:, :, G:]) and torch.equal(lse[:, G:], want_lse[:, G:])
+    w = torch.from_numpy(_host(kv, cache).weight)[0]
+    assert torch.isnan(w[0, :n]).all() and not torch.isnan(w[1, :n]).any()
+    U.ulysses_kv4_attn(kv, cache, q, out, _i32([0], gpu), SCALE, lse=lse, workspace=ws)
+    assert not bool(out.any()) and bool((lse == float("-inf")).all())

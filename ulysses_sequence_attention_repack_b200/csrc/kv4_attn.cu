@@ -279,19 +279,27 @@ struct Feed {
   }
 };
 
-// Row r of (sequence b, K/V head h): four dims a lane of the warp, from its sum
-// o, its sum of p and its maximum.
-__device__ __forceinline__ float row_log2(float sum, float M) { return sum == 0.f ? NEG_INF : M + log2f(sum); }
+// The log-sum of row r of a sequence of len slots, from its sum of p and its
+// maximum.  A sum of 0 is a row that sees no slot, or one whose logits are all
+// -infinity, past the range of fp32: that one has no softmax.
+__device__ __forceinline__ float row_log2(const Args& a, int len, int r, float sum, float M) {
+  if (sum == 0.f) return row_limit(a, len, r) > 0 ? __int_as_float(0x7fc00000) : NEG_INF;
+  return M + log2f(sum);
+}
 
-__device__ __forceinline__ void finish_row(const Args& a, int b, int h, int r, int lane, float4 o, float sum, float M) {
+// Row r of (sequence b of len slots, K/V head h): four dims a lane of the warp,
+// from its sum o, its sum of p and its maximum.
+__device__ __forceinline__ void finish_row(const Args& a, int b, int len, int h, int r, int lane, float4 o, float sum,
+                                           float M) {
   const int i = r / a.G, hq = h * a.G + (r - i * a.G);
-  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const float log_sum = row_log2(a, len, r, sum, M);
+  const float f = sum == 0.f ? (log_sum == NEG_INF ? 0.f : log_sum) : 1.f / sum;
   uint2 y;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.x) : "f"(o.y * f), "f"(o.x * f));
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.y) : "f"(o.w * f), "f"(o.z * f));
   const int64_t row = (static_cast<int64_t>(b) * a.Lq + i) * a.H * a.G + hq;
   reinterpret_cast<uint2*>(a.out + row * kKv4Dim)[lane] = y;
-  if (a.lse && lane == 0) a.lse[(static_cast<int64_t>(b) * a.H * a.G + hq) * a.Lq + i] = row_log2(sum, M);
+  if (a.lse && lane == 0) a.lse[(static_cast<int64_t>(b) * a.H * a.G + hq) * a.Lq + i] = log_sum;
 }
 
 // ---------------------------------------------------------------- main kernel
@@ -907,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       }
       const int r = row0 + row;
       if (whole) {
-        finish_row(a, b, h, r, lane, o, sum, Mt);
+        finish_row(a, b, len, h, r, lane, o, sum, Mt);
         if (kWeights && lane == 0) a.row_ml[bh * a.R + r] = make_float2(Mt, sum);
       } else {
         reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(part) * RPB + row) * kKv4Dim)[lane] = o;
@@ -1029,11 +1037,13 @@ __device__ __forceinline__ Sum join_parts(const Args& a, const Parts& p, int row
 // Blocks below `row_blocks` join `rpb` rows each: a warp a row, or, where a row
 // was cut into more than kWarpParts parts, all warps one after another.
 // Further blocks: kWeightSlots slots of a pair each,
-// weight_t += sum_r 2^(z_rt - lse_r), the rows in their order.
+// weight_t += sum_r 2^(z_rt - lse_r), the rows in their order.  Four blocks an SM
+// (64 registers; with 74 and three, 24 ragged sequences x 8 heads with 7 rows
+// and weights: 50.2 -> 53.7 us).
 constexpr int kWarpParts = 8;
 
 template <int RPB>
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, int ctas, int rpb, int64_t rows,
+__global__ void __launch_bounds__(kJoinThreads, 4) kv4_join_kernel(const Args a, int ctas, int rpb, int64_t rows,
                                                                 int64_t row_blocks) {
   __shared__ __align__(16) float so[kJoinWarps][kKv4Dim];
   __shared__ float2 sml[kJoinWarps];
@@ -1045,15 +1055,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, in
   const int64_t x = blockIdx.x;
   const int chunk = tiles_per_cta(total_tiles(a, false), ctas);
   if (x < row_blocks) {
-    const auto parts_of = [&](int64_t i, int* b, int* h, int* r) {   // of row i; ntiles 0: it sees no slot
+    const auto parts_of = [&](int64_t i, int* b, int* len, int* h, int* r) {   // of row i
       const int64_t bh = i / a.R;
       *r = static_cast<int>(i - bh * a.R);
       *b = static_cast<int>(bh / a.H);
       *h = static_cast<int>(bh - static_cast<int64_t>(*b) * a.H);
-      const int ntiles = tiles_of(kv4_length(a.lengths[*b], a.cap, nullptr));
-      return Parts(chunk, ctas, first_tile(a, *b), *h * a.RB + *r / RPB, ntiles);
+      *len = kv4_length(a.lengths[*b], a.cap, nullptr);
+      return Parts(chunk, ctas, first_tile(a, *b), *h * a.RB + *r / RPB, tiles_of(*len));
     };
-    const auto all_warps = [&](const Parts& p, int b, int h, int r) {
+    const auto all_warps = [&](const Parts& p, int b, int len, int h, int r) {
       const Sum mine = join_parts<RPB>(a, p, r % RPB, warp, kJoinWarps);
       reinterpret_cast<float4*>(so[warp])[lane] = mine.o;
       if (lane == 0) sml[warp] = make_float2(mine.M, mine.p);
@@ -1066,32 +1076,32 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, in
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w)
           all.add(ex2(sml[w].x - base), reinterpret_cast<const float4*>(so[w])[lane], sml[w].y);
-        finish_row(a, b, h, r, lane, all.o, all.p, all.M);
+        finish_row(a, b, len, h, r, lane, all.o, all.p, all.M);
       }
     };
     const int64_t i0 = x * rpb, mine = rpb == 1 ? i0 : i0 + warp;
-    int b, h, r;
+    int b, len, h, r;
     if (lane == 0) shared_row[warp] = 0;
     if (mine < rows) {
-      const Parts p = parts_of(mine, &b, &h, &r);
+      const Parts p = parts_of(mine, &b, &len, &h, &r);
       const int n = p.c1 - p.c0 + 1;
       if (p.empty) {
-        if (rpb > 1 || warp == 0) finish_row(a, b, h, r, lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, NEG_INF);
+        if (rpb > 1 || warp == 0) finish_row(a, b, 0, h, r, lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, NEG_INF);
       } else if (rpb == 1) {
-        if (n > 1) all_warps(p, b, h, r);
+        if (n > 1) all_warps(p, b, len, h, r);
       } else if (n > kWarpParts) {
         if (lane == 0) shared_row[warp] = 1;
       } else if (n > 1) {
         const Sum s = join_parts<RPB>(a, p, r % RPB, 0, 1);
-        finish_row(a, b, h, r, lane, s.o, s.p, s.M);
+        finish_row(a, b, len, h, r, lane, s.o, s.p, s.M);
       }
     }
     if (rpb == 1) return;
     __syncthreads();
     for (int v = 0; v < rpb; ++v) {
       if (!shared_row[v]) continue;
-      const Parts p = parts_of(i0 + v, &b, &h, &r);
-      all_warps(p, b, h, r);
+      const Parts p = parts_of(i0 + v, &b, &len, &h, &r);
+      all_warps(p, b, len, h, r);
       __syncthreads();
     }
     return;
@@ -1110,7 +1120,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Args a, in
     if (r < a.R) {
       const Parts p(chunk, ctas, first, h * a.RB + r / RPB, ntiles);
       const float2 ml = p.c0 == p.c1 ? a.row_ml[bh * a.R + r] : join_ml<RPB>(a, p, r % RPB);
-      if (lane == 0) slse[warp] = row_log2(ml.y, ml.x);
+      if (lane == 0) slse[warp] = row_log2(a, len, r, ml.y, ml.x);
     }
     __syncthreads();
 #pragma unroll 2
