@@ -599,9 +599,18 @@ size_t ulysses_kv4_attn_workspace_bytes(const ulysses_kv4_t* kv, int32_t q_heads
  * row that sees no slot gives zeros and -infinity; one that sees some, of a q
  * row that holds an infinity, a NaN or a magnitude of 2^115 or more, or whose
  * logits leave the range of fp32 (one above it, or all below), gives NaN.
- * With ULYSSES_KV4_WEIGHTS, weights[b, h, t] += the sum of slot t's softmax weights over the rows of head
- * h.  fp32 logits, softmax and sums; weights times scales in fp16 for the second
- * product.  Meant for few rows (1 to about 16 = G * q_len); more work, each
+ * With ULYSSES_KV4_WEIGHTS, weights[b, h, t] += the sum of slot t's softmax
+ * weights over the rows of head h that see it.
+ *
+ * Precision: fp32 logits, softmax and sums.  q's values keep their 8 bits down
+ * to 2^-28 of the power of two of their row's largest, and fewer below it.  A
+ * weight times a step is rounded to fp16 for the second product: by 2^-11 of
+ * itself, or by 2^-30 of the largest such product that the row meets in that
+ * group, whichever is more.  Sums over V are divided by the sum of the weights
+ * at the end: where |V| times 256 times the slots passes 2^127, they may not
+ * be finite.
+ *
+ * Meant for few rows (1 to about 16 = G * q_len); more work, each
  * further 16 reading the cache again.  Errors: ARG, ALIGN, DIVISIBILITY
  * (q_heads % heads), WORKSPACE, UNSUPPORTED, CUDA.
  */

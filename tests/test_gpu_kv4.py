@@ -1118,3 +1118,20 @@ def test_logits_past_the_range_of_fp32_give_nan(gpu, q_len, G, sign):
     assert torch.isnan(w[0, :n]).all() and not torch.isnan(w[1, :n]).any()
     U.ulysses_kv4_attn(kv, cache, q, out, _i32([0], gpu), SCALE, lse=lse, workspace=ws)
     assert not bool(out.any()) and bool((lse == float("-inf")).all())
+
+
+@pytest.mark.parametrize("q_len,G", SHAPES)
+def test_small_query_values_keep_their_bits(gpu, q_len, G):
+    """Values down to 2^-28 of the power of two of their row's largest enter with all 8 bits: a query whose second
+    group is that small against keys whose second group is as much larger (and whose first is 0)."""
+    n = 90
+    kv, cache, k, v = _make(gpu, [n], 2, 96, 150)
+    q = _queries(gpu, 1, q_len, 2 * G, 151)
+    small = q[..., 64:].abs().clamp(1, 1.9921875) * q[..., 64:].sign()
+    q[..., :64] = 0
+    q[..., 0] = 1.9921875
+    q[..., 64:] = small * 2.0 ** -28
+    k[..., :64] = 0
+    k[..., 64:] *= 2.0 ** 28
+    U.ulysses_kv4_append(kv, cache, k, v, _i32([0, n], gpu), _i32([0], gpu))
+    _attend(gpu, kv, cache, q, [n], True)

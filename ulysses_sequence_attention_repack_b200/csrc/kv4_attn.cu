@@ -26,9 +26,10 @@
 //   that is large in a slot with hardly any weight, or in one that the row does
 //   not see, costs its other slots nothing.
 //
-// Roundings: q, codes, scales and minima enter exactly (q by a power of two,
-// which keeps its 8 bits down to 2^-28 of the row's largest); z, p, maxima and
-// sums are fp32; p s is rounded to fp16 for the second product, off by at most
+// Roundings: codes, scales and minima enter exactly, and q by a power of two
+// that takes its row's largest just below fp16's end: 8 bits down to 2^-28 of
+// that (of its power of two; a sixteenth of an odd value is 2^-17 there, whose
+// last bit is fp16's least, 2^-24), fewer below; z, p, maxima and sums are fp32; p s is rounded to fp16 for the second product, off by at most
 // 2^-11 of itself (bf16's 2^-8 would show in o) and, since the row's largest p s
 // sits at 2^5 or more, by 2^-30 of that for the smallest; o is rounded once, to
 // bf16.
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
 
     // the query as the second operand of z^T = K q^T: this lane holds, of row
     // row0 + 8 nt + g, dims 16t .. 16t + 15 of each group, scaled by a power of
-    // two that takes the row's largest into [2^14, 2^15)
+    // two that takes the row's largest into [2^15, 2^16) (65,280 at most)
     uint32_t qf[NT][16];
     float qscale[NT][2], qsum[NT][2][2];
     int limit[NT][2];
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int k = static_cast<int>(top >> 23) - 127;
-      const int e = max(-100, min(126, 14 - k));
+      const int e = max(-100, min(126, 15 - k));
       const float up = pow2(e);
       float sum[2] = {0.f, 0.f};
 #pragma unroll
