@@ -35,6 +35,11 @@ def test_plan_refusals():
     assert U.load().ulysses_kv4_plan(None, 1, 1, 128, 32) == _lib.ULYSSES_ERR_ARG
 
 
+def test_a_capacity_does_not_wrap_into_64_bits():
+    assert _code(1, 1, 128, (1 << 64) + 32) == _lib.ULYSSES_ERR_ALIGN   # held at 2^63 - 1
+    assert _code(1, 1, 128, -(1 << 64) + 32) == _lib.ULYSSES_ERR_ARG
+
+
 @pytest.mark.parametrize("B,H,cap", [(1, 1, 32), (3, 8, 1024), (1, 56, 104448), (24, 8, 8192)])
 def test_sizes(B, H, cap):
     kv = U.ulysses_kv4_plan(B, H, 128, cap)

@@ -531,8 +531,8 @@ def ulysses_kv4_plan(batch: int, heads: int, D: int, capacity: int) -> KV4Plan:
     """The geometry of 4-bit K/V caches: `capacity` slots (a multiple of 32)
     for each of `batch` sequences and `heads` K/V heads of D = 128."""
     h = ctypes.c_void_p()
-    _check(load().ulysses_kv4_plan(ctypes.byref(h), _kv4_int(batch), _kv4_int(heads), _kv4_int(D), int(capacity)),
-           "ulysses_kv4_plan")
+    _check(load().ulysses_kv4_plan(ctypes.byref(h), _kv4_int(batch), _kv4_int(heads), _kv4_int(D),
+                                   max(-1, min(int(capacity), 2 ** 63 - 1))), "ulysses_kv4_plan")
     return KV4Plan(h.value, int(batch), int(heads), int(D), int(capacity))
 
 
