@@ -129,3 +129,72 @@ def test_range_check_refuses_and_reports(gpu):
     assert lib.ulysses_selftest_bounds_check(err.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert int(err[0].item()) == 4 | 0x10 | 0x20 | 0x40, hex(int(err[0].item()))
+
+
+# The 4-bit cache's calls at odd sizes, saved as above.
+_KV4_SCRIPT = r"""
+import sys
+import numpy as np
+import torch
+sys.path.insert(0, sys.argv[3])
+import ulysses_sequence_attention_repack_b200 as U
+dev = torch.device("cuda", 0)
+g = torch.Generator(device=dev)
+g.manual_seed(93)
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+out, err = {}, 0
+
+# K and V as planes of a head slab of two ranks, behind what is cached; slots and rows of no sequence at the ends
+lens, start, heads, cap = [97, 0, 5000, 1], [3, 0, 11, 31], 4, 5024
+n = sum(lens)
+T = torch.randn((2, 3, n + 5, heads // 2, 128), generator=g, device=dev).to(torch.bfloat16)
+kv = U.ulysses_kv4_plan(len(lens), heads, 128, cap)
+cache = torch.zeros(kv.cache_bytes, dtype=torch.uint8, device=dev)
+cu = i32([0, *np.cumsum(lens).tolist()])
+U.ulysses_kv4_append(kv, cache, T[:, 1], T[:, 2], cu, i32(start), i32([7, 8, 9, 10]))
+back = torch.zeros_like(T)
+U.ulysses_kv4_load(kv, cache, back[:, 1], back[:, 2], cu, i32(start))
+few = torch.zeros((4, heads, 128), dtype=torch.bfloat16, device=dev)       # a token a sequence: the other form
+U.ulysses_kv4_load(kv, cache, few, torch.empty_like(few), i32([0, 1, 2, 3, 4]), i32([0, 0, 5023, 31]))
+out["back"], out["few"] = back, few
+ln = i32([100, 0, 5011, 32])
+for q_len, G in ((1, 1), (2, 1), (1, 5), (3, 3), (20, 1)):
+    wide = torch.randn((4, q_len, heads * G + 1, 128), generator=g, device=dev).to(torch.bfloat16)
+    for weights in (False, True):
+        o = torch.zeros((4, q_len, heads * G, 128), dtype=torch.bfloat16, device=dev)
+        lse = torch.zeros((4, heads * G, q_len), device=dev)
+        ws = torch.empty(kv.workspace_bytes(heads * G, q_len, weights), dtype=torch.uint8, device=dev)
+        U.ulysses_kv4_attn(kv, cache, wide[:, :, 1:], o, ln, 0.09, lse=lse, causal=True, weights=weights, workspace=ws)
+        out[f"o{q_len}-{G}-{int(weights)}"], out[f"l{q_len}-{G}-{int(weights)}"] = o, lse
+out["cache"] = cache
+small = U.ulysses_kv4_plan(len(lens), heads, 128, 96)
+kept, new = torch.zeros(small.cache_bytes, dtype=torch.uint8, device=dev), i32([0] * 4)
+U.ulysses_kv4_evict(kv, cache, small, kept, ln, new, 70, 3, 20)
+out["kept"], out["new"] = kept, new
+# pairs of more slots than a block holds the keys of
+many = U.ulysses_kv4_plan(1, 296, 128, 22560)
+cache = torch.zeros(many.cache_bytes, dtype=torch.uint8, device=dev)
+at = many.weight_offset
+cache[at:many.position_offset].view(torch.float32).copy_(torch.rand(296 * 22560, generator=g, device=dev))
+cache[many.position_offset:].view(torch.int32).copy_(torch.arange(296 * 22560, device=dev))
+to = U.ulysses_kv4_plan(1, 296, 128, 64)
+kept, new = torch.zeros(to.cache_bytes, dtype=torch.uint8, device=dev), i32([0])
+U.ulysses_kv4_evict(many, cache, to, kept, i32([22541]), new, 50, 4, 9)
+out["kept_many"], out["new_many"] = kept, new
+torch.cuda.synchronize()
+for p in (kv, small, many, to):
+    err |= U.ulysses_kv4_last_device_error(p)
+save = {k: v.contiguous().view(torch.uint8).cpu().numpy() for k, v in out.items()}
+np.savez(sys.argv[1], err=np.array([err]), **save)
+"""
+
+
+def test_debug_build_runs_the_4_bit_cache_clean_and_matches(gpu, tmp_path, monkeypatch):
+    from ulysses_sequence_attention_repack_b200 import build
+    monkeypatch.setitem(globals(), "_SCRIPT", _KV4_SCRIPT)
+    got = _run(tmp_path, build.ensure_debug_built(), (), "debug")
+    want = _run(tmp_path, None, (), "release")
+    assert int(got["err"][0]) == 0, hex(int(got["err"][0]))
+    assert int(want["err"][0]) == 0
+    for name in want:
+        assert np.array_equal(got[name], want[name]), name

@@ -3,9 +3,9 @@
 Usage: python -m ulysses_sequence_attention_repack_b200.build [--debug]
 
 --debug builds libulysses_debug.so instead: the same library compiled with
--DULYSSES_DEBUG, whose repack, prologue, push and attention-epilogue kernels
-range-check every computed global offset (an access outside its buffer is
-skipped and reported through the device error word).  Select it at run time
+-DULYSSES_DEBUG, whose repack, prologue, push, attention-epilogue and 4-bit
+cache kernels range-check every computed global offset (an access outside its
+buffer is skipped and reported through the device error word).  Select it at run time
 with ULYSSES_LIBRARY=<path> (see _lib.load).
 """
 from __future__ import annotations

@@ -99,6 +99,15 @@ struct Args {
   float scale_log2;
   int32_t causal;
   unsigned int* err;
+
+  // extents, for the bounds-checked build
+  __device__ int64_t slots() const { return static_cast<int64_t>(B) * H * cap; }
+  __device__ int64_t blocks_bytes() const { return slots() / kKv4BlockSlots * kKv4BlockBytes; }
+  __device__ int64_t rows() const { return static_cast<int64_t>(B) * H * R; }
+  __device__ int64_t q_extent() const {
+    return (static_cast<int64_t>(B) * Lq - 1) * q_token_stride + (static_cast<int64_t>(H) * G - 1) * q_head_stride +
+           kKv4Dim;
+  }
 };
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -194,6 +203,12 @@ __device__ __forceinline__ int first_tile(const Args& a, int b) {
   return __reduce_add_sync(0xffffffffu, n) * a.H * a.RB;
 }
 
+// Rows of unfinished sums in the workspace: two of a block of RPB a CTA.
+template <int RPB>
+__host__ __device__ constexpr int64_t part_rows() {
+  return static_cast<int64_t>(2) * kMaxCtas * RPB;
+}
+
 // A place in the list: tile `lo` of `ntiles` of unit (head, row block) `unit` of sequence b.
 struct Place {
   int b, len, ntiles, unit, lo;
@@ -264,9 +279,13 @@ struct Feed {
       if (exists) {
         if (lane == 0) {
           const uint32_t s = issued % kStages, bar = bars + 8 * s;
-          mbar_arrive_expect_tx(bar, kKv4BlockBytes);
-          bulk_load(ring + s * kKv4BlockBytes, pair + static_cast<int64_t>(block) * kKv4BlockBytes, kKv4BlockBytes,
-                    bar);
+          const uint8_t* from = pair + static_cast<int64_t>(block) * kKv4BlockBytes;
+          if (in_bounds(from - a.cache, kKv4BlockBytes, a.blocks_bytes(), a.err)) {
+            mbar_arrive_expect_tx(bar, kKv4BlockBytes);
+            bulk_load(ring + s * kKv4BlockBytes, from, kKv4BlockBytes, bar);
+          } else {
+            mbar_arrive(bar);
+          }
         }
         ++issued;
       }
@@ -299,8 +318,9 @@ __device__ __forceinline__ void finish_row(const Args& a, int b, int len, int h,
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.x) : "f"(o.y * f), "f"(o.x * f));
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.y) : "f"(o.w * f), "f"(o.z * f));
   const int64_t row = (static_cast<int64_t>(b) * a.Lq + i) * a.H * a.G + hq;
-  reinterpret_cast<uint2*>(a.out + row * kKv4Dim)[lane] = y;
-  if (a.lse && lane == 0) a.lse[(static_cast<int64_t>(b) * a.H * a.G + hq) * a.Lq + i] = log_sum;
+  store_at(reinterpret_cast<uint2*>(a.out), row * (kKv4Dim / 4) + lane, a.rows() * (kKv4Dim / 4), y, a.err);
+  if (a.lse && lane == 0)
+    store_at(a.lse, (static_cast<int64_t>(b) * a.H * a.G + hq) * a.Lq + i, a.rows(), log_sum, a.err);
 }
 
 // ---------------------------------------------------------------- main kernel
@@ -402,13 +422,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       float f[2][16];
       if (r < a.R) {
         const int i = r / a.G;
-        const uint16_t* src = a.q + (static_cast<int64_t>(b) * a.Lq + i) * a.q_token_stride +
-                              static_cast<int64_t>(h * a.G + (r - i * a.G)) * a.q_head_stride;
+        const int64_t at = (static_cast<int64_t>(b) * a.Lq + i) * a.q_token_stride +
+                           static_cast<int64_t>(h * a.G + (r - i * a.G)) * a.q_head_stride + 16 * t;
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + 64 * w + 16 * t + 8 * v);
+            const uint4 x = load_at(reinterpret_cast<const uint4*>(a.q), at / 8 + 8 * w + v, a.q_extent() / 8,
+                                    make_uint4(0, 0, 0, 0), a.err);
             const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -621,7 +642,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
         z[r] = x;
         weigh(r);
         move |= x > rM[r] + kGrow || ps[r][0] > kMost || ps[r][1] > kMost;
-        if (kWeights && r < a.R && (!kEdge || slot < len)) a.logits[(bh * a.R + r) * a.cap + slot] = x;
+        if (kWeights && r < a.R && (!kEdge || slot < len))
+          store_at(a.logits, (bh * a.R + r) * a.cap + slot, a.rows() * a.cap, x, a.err);
       }
       if (__any_sync(0xffffffffu, move)) {
         float fac[2][2] = {{1.f, 1.f}, {1.f, 1.f}};   // of this lane's columns of o^T, in each group
@@ -712,7 +734,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
               if (kWeights) {
                 const int r = row0 + 8 * nt + 2 * t + row;
                 const float z = kEdge && slot >= limit[nt][row] ? NEG_INF : x * qscale[nt][row];
-                if (r < a.R && (!kEdge || slot < len)) a.logits[(bh * a.R + r) * a.cap + slot] = z;
+                if (r < a.R && (!kEdge || slot < len))
+                  store_at(a.logits, (bh * a.R + r) * a.cap + slot, a.rows() * a.cap, z, a.err);
               }
             }
         }
@@ -917,10 +940,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
       const int r = row0 + row;
       if (whole) {
         finish_row(a, b, len, h, r, lane, o, sum, Mt);
-        if (kWeights && lane == 0) a.row_ml[bh * a.R + r] = make_float2(Mt, sum);
+        if (kWeights && lane == 0) store_at(a.row_ml, bh * a.R + r, a.rows(), make_float2(Mt, sum), a.err);
       } else {
-        reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(part) * RPB + row) * kKv4Dim)[lane] = o;
-        if (lane == 0) a.part_ml[part * RPB + row] = make_float2(Mt, sum);
+        store_at(reinterpret_cast<float4*>(a.part_o), (static_cast<int64_t>(part) * RPB + row) * (kKv4Dim / 4) + lane,
+                 part_rows<RPB>() * (kKv4Dim / 4), o, a.err);
+        if (lane == 0) store_at(a.part_ml, part * RPB + row, part_rows<RPB>(), make_float2(Mt, sum), a.err);
       }
     }
     __syncthreads();
@@ -966,7 +990,7 @@ __device__ __forceinline__ float2 join_ml(const Args& a, const Parts& p, int row
   const int lane = threadIdx.x & 31;
   float M = NEG_INF, sum = 0.f;
   for (int c = p.c0 + lane; c <= p.c1; c += 32) {
-    const float2 x = a.part_ml[p.part(c) * RPB + row];
+    const float2 x = load_at(a.part_ml, p.part(c) * RPB + row, part_rows<RPB>(), make_float2(NEG_INF, 0.f), a.err);
     const float m = fmaxf(M, x.x);
     const float base = m == NEG_INF ? 0.f : m;
     sum = sum * ex2(M - base) + x.y * ex2(x.x - base);
@@ -1019,8 +1043,9 @@ __device__ __forceinline__ Sum join_parts(const Args& a, const Parts& p, int row
       y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c + u * step <= p.c1) {
         const int64_t at = static_cast<int64_t>(p.part(c + u * step)) * RPB + row;
-        ml[u] = a.part_ml[at];
-        y[u] = reinterpret_cast<const float4*>(a.part_o + at * kKv4Dim)[lane];
+        ml[u] = load_at(a.part_ml, at, part_rows<RPB>(), ml[u], a.err);
+        y[u] = load_at(reinterpret_cast<const float4*>(a.part_o), at * (kKv4Dim / 4) + lane,
+                       part_rows<RPB>() * (kKv4Dim / 4), y[u], a.err);
       }
     }
     float m = s.M;
@@ -1120,18 +1145,22 @@ __global__ void __launch_bounds__(kJoinThreads, 4) kv4_join_kernel(const Args a,
     const int r = r0 + warp;   // each warp finds one row's log-sum
     if (r < a.R) {
       const Parts p(chunk, ctas, first, h * a.RB + r / RPB, ntiles);
-      const float2 ml = p.c0 == p.c1 ? a.row_ml[bh * a.R + r] : join_ml<RPB>(a, p, r % RPB);
+      const float2 ml = p.c0 == p.c1
+                            ? load_at(a.row_ml, bh * a.R + r, a.rows(), make_float2(NEG_INF, 0.f), a.err)
+                            : join_ml<RPB>(a, p, r % RPB);
       if (lane == 0) slse[warp] = row_log2(a, len, r, ml.y, ml.x);
     }
     __syncthreads();
 #pragma unroll 2
     for (int i = 0; i < min(kJoinWarps, a.R - r0); ++i) {
       const float lse = slse[i];
-      const float* z = a.logits + (bh * a.R + r0 + i) * a.cap + slot0;
+      const int64_t z = ((bh * a.R + r0 + i) * a.cap + slot0) / 4;
       float4 v[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (slot0 + k * (kWeightSlots / 2) < len) v[k] = *reinterpret_cast<const float4*>(z + k * (kWeightSlots / 2));
+        if (slot0 + k * (kWeightSlots / 2) < len)
+          v[k] = load_at(reinterpret_cast<const float4*>(a.logits), z + k * (kWeightSlots / 8), a.rows() * a.cap / 4,
+                         make_float4(0.f, 0.f, 0.f, 0.f), a.err);
       if (lse == NEG_INF) continue;
       if (lse != lse) {   // a row without a softmax: no number for the slots it sees, nothing for the others
         const int limit = row_limit(a, len, r0 + i);
@@ -1158,6 +1187,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) kv4_join_kernel(const Args a,
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int64_t slot = slot0 + k * (kWeightSlots / 2);
+    if (slot < len && !in_bounds(bh * a.cap + slot, 4, a.slots(), a.err)) continue;
     float* f = a.weight + bh * a.cap + slot;   // (16-byte aligned: capacities are multiples of 32)
     if (slot + 3 < len) {
       const float4 v = *reinterpret_cast<float4*>(f);

@@ -101,6 +101,15 @@ __device__ __forceinline__ int64_t row_offset(const Kv4Rows& r, int64_t i, int h
   return i * r.token_stride + rank * r.rank_stride + (h - rank * r.heads_per_rank) * r.head_stride;
 }
 
+// Elements from the first row's to the last one's end, and slots of the cache (for the bounds-checked build).
+__device__ __forceinline__ int64_t row_extent(const Kv4Rows& r, int H) {
+  return (r.rows - 1) * r.token_stride + (r.heads_per_rank - 1) * r.head_stride +
+         (H / r.heads_per_rank - 1) * r.rank_stride + kKv4Dim;
+}
+__device__ __forceinline__ int64_t slots_of(int B, int H, int64_t capacity) {
+  return static_cast<int64_t>(B) * H * capacity;
+}
+
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowsLaunc
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[plane][i] = make_uint4(0, 0, 0, 0);
-      if (i0 + u < a.rows32) {
+      if (i0 + u < a.rows32 && in_bounds(row + 32 * i, 8, row_extent(a.r, a.H), a.err)) {
         const int4 v = ld_stream(reinterpret_cast<const int4*>(static_cast<const uint16_t*>(plane ? a.r.v : a.r.k) +
                                                                row + 32 * i));
         x[plane][i] = make_uint4(v.x, v.y, v.z, v.w);
@@ -242,9 +251,11 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4RowsLaunc
   const int64_t m_off = blk + kKv4MetaOffset + at * 16;
   if (q == 0 && in_bounds(m_off, 16, a.blocks_bytes, a.err))
     *reinterpret_cast<uint4*>(a.cache + m_off) = make_uint4(meta[0][0], meta[0][1], meta[1][0], meta[1][1]);
-  if (q == 1) a.weight[bh * a.cap + slot] = 0.f;
+  const int64_t slots = slots_of(a.B, a.H, a.cap);
+  if (q == 1) store_at(a.weight, bh * a.cap + slot, slots, 0.f, a.err);
   if (q == 2)
-    a.pos[bh * a.cap + slot] = static_cast<int32_t>(a.r.pos0 ? a.r.pos0[b] + (slot - a.r.start[b]) : slot);
+    store_at(a.pos, bh * a.cap + slot, slots,
+             static_cast<int32_t>(a.r.pos0 ? a.r.pos0[b] + (slot - a.r.start[b]) : slot), a.err);
 }
 
 // bf16(m + s n) of the 8 codes of a word: a nibble under the exponent of 2^7 is
@@ -273,7 +284,9 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const Kv4RowsLaunch 
   if (item >= a.items) return;
   const int plane = lane >> 4, l16 = lane & 15;
   const int c_at = plane * kKv4VOffset + (l16 & 7) * 8 + (l16 >> 3) * 4, m_at = plane * 8 + (l16 >> 3) * 4;
-  uint16_t* dst = static_cast<uint16_t*>(plane ? a.r.v : a.r.k) + row_offset(a.r, i0, h, a.H) + l16 * 8;
+  uint4* dst = static_cast<uint4*>(plane ? a.r.v : a.r.k);
+  const int64_t to = row_offset(a.r, i0, h, a.H) / 8 + l16, step = a.r.token_stride / 8;
+  const int64_t extent = row_extent(a.r, a.H) / 8;
   const RowPlace mine = place_rows<T>(a.r, a.rows32, i0, a.B, a.cap, a.err);
   if (one_run<T>(mine)) {
     const int64_t slot0 = __shfl_sync(0xffffffffu, mine.slot, 0);
@@ -290,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const Kv4RowsLaunch 
     }
 #pragma unroll
     for (int u = 0; u < T; ++u)
-      *reinterpret_cast<uint4*>(dst + u * a.r.token_stride) = dequantise(code[u], meta[u]);
+      store_at(dst, to + u * step, extent, dequantise(code[u], meta[u]), a.err);
   } else if (T > 1) {
 #pragma unroll 1
     for (int u = 0; u < T; ++u) {
@@ -301,9 +314,10 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const Kv4RowsLaunch 
       const int at = static_cast<int>(slot % kKv4BlockSlots);
       const int64_t off = blk + (code_row(at) + c_at), m_off = blk + (meta_row(at) + m_at);
       if (in_bounds(off, 4, a.blocks_bytes, a.err) && in_bounds(m_off, 4, a.blocks_bytes, a.err))
-        *reinterpret_cast<uint4*>(dst + u * a.r.token_stride) =
-            dequantise(*reinterpret_cast<const uint32_t*>(a.cache + off),
-                       *reinterpret_cast<const uint32_t*>(a.cache + m_off));
+        store_at(dst, to + u * step, extent,
+                 dequantise(*reinterpret_cast<const uint32_t*>(a.cache + off),
+                            *reinterpret_cast<const uint32_t*>(a.cache + m_off)),
+                 a.err);
     }
   }
 }
@@ -377,21 +391,25 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
   const int n = kv4_length(a.lengths[b], a.src_cap, threadIdx.x == 0 ? a.err : nullptr);
   const int kept = n < a.keep ? n : a.keep;
   if (bh - static_cast<int64_t>(b) * a.H == 0 && rank == 0 && threadIdx.x == 0) a.new_lengths[b] = kept;
-  int32_t* idx = a.dst_pos + bh * a.dst_cap;
+  const auto put = [&](int64_t j, int i) {   // the pair's kept slot j is slot i
+    if (in_bounds(j, 1, a.keep, a.err))
+      store_at(a.dst_pos, bh * a.dst_cap + j, slots_of(a.B, a.H, a.dst_cap), i, a.err);
+  };
   const int run = ((n + cluster - 1) / cluster + 3) / 4 * 4;   // a multiple of 4: 16-byte loads of weights
   const int i_begin = min(n, rank * run), i_end = min(n, i_begin + run);
   if (n <= a.keep) {   // (the whole cluster)
-    for (int j = i_begin + threadIdx.x; j < i_end; j += blockDim.x) idx[j] = j;
+    for (int j = i_begin + threadIdx.x; j < i_end; j += blockDim.x) put(j, j);
     return;
   }
-  const float* w = a.src_weight + bh * a.src_cap;
+  const int64_t w = bh * a.src_cap, slots = slots_of(a.B, a.H, a.src_cap);   // the pair's weights
   const int c0 = a.sink, c1 = n - a.recent;   // slots outside [c0, c1) are protected
   // The keys of slots i .. i + 3 (capacities are multiples of 4: the load stays
   // inside the pair).  Slots behind the length, which follow the very last
   // one only, get the lowest key: the first of its equals are kept, and there
   // are enough of them before these.
   const auto make_keys = [&](int i) {
-    const float4 v = *reinterpret_cast<const float4*>(w + i);
+    const float4 v = load_at(reinterpret_cast<const float4*>(a.src_weight), (w + i) / 4, slots / 4,
+                             make_float4(0.f, 0.f, 0.f, 0.f), a.err);
     uint32_t k[4] = {weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w)};
     if (i < c0 || i + 3 >= c1) {
 #pragma unroll
@@ -410,7 +428,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
     if constexpr (kHeld)
       return held[i - i_begin];
     else
-      return i < c0 || i >= c1 ? 0xffffffffu : weight_key(w[i]);
+      return i < c0 || i >= c1 ? 0xffffffffu : weight_key(load_at(a.src_weight, w + i, slots, 0.f, a.err));
   };
   __syncthreads();
 
@@ -515,7 +533,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictL
     const uint32_t is_equal = __ballot_sync(0xffffffffu, equal_here);
     const uint32_t q = equal_before + __popc(is_equal & below);
     if (k > prefix || (equal_here && q < left))
-      idx[keep_before + __popc(is_sure & below) + min(q, left)] = i;
+      put(keep_before + __popc(is_sure & below) + min(q, left), i);
     keep_before += __popc(is_sure);
     equal_before += __popc(is_equal);
   }
@@ -540,11 +558,15 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4EvictLaun
   const int kept = n < a.keep ? n : a.keep;
   const int lane = threadIdx.x & 31, part = lane & 7;
   const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kGatherSlots + (threadIdx.x >> 5) * 4 * kMoves + (lane >> 3);
-  int32_t* dpos = a.dst_pos + bh * a.dst_cap;
+  const int64_t to = bh * a.dst_cap, from = bh * a.src_cap;   // the pair's first slots
+  const int64_t src_slots = slots_of(a.B, a.H, a.src_cap), dst_slots = slots_of(a.B, a.H, a.dst_cap);
   const int c_at = (part >> 2) * kKv4VOffset + (part & 3) * 16;
   int32_t src[kMoves];
 #pragma unroll
-  for (int u = 0; u < kMoves; ++u) src[u] = j0 + 4 * u < kept ? dpos[j0 + 4 * u] : -1;
+  for (int u = 0; u < kMoves; ++u) {
+    src[u] = j0 + 4 * u < kept ? load_at(a.dst_pos, to + j0 + 4 * u, dst_slots, -1, a.err) : -1;
+    if (src[u] >= 0 && !in_bounds(src[u], 1, a.src_cap, a.err)) src[u] = -1;
+  }
   int4 codes[kMoves], meta[kMoves];
   int32_t word[kMoves];
 #pragma unroll
@@ -556,20 +578,20 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4EvictLaun
     const int at = src[u] % kKv4BlockSlots;
     codes[u] = ld_stream(reinterpret_cast<const int4*>(blk + c_at + at * 64));
     if (part == 0) meta[u] = ld_stream(reinterpret_cast<const int4*>(blk + kKv4MetaOffset + at * 16));
-    if (part == 1) word[u] = __float_as_int(a.src_weight[bh * a.src_cap + src[u]]);
-    if (part == 2) word[u] = a.src_pos[bh * a.src_cap + src[u]];
+    if (part == 1) word[u] = __float_as_int(load_at(a.src_weight, from + src[u], src_slots, 0.f, a.err));
+    if (part == 2) word[u] = load_at(a.src_pos, from + src[u], src_slots, 0, a.err);
   }
   __syncwarp();   // every lane has its slot numbers before positions replace them
 #pragma unroll
   for (int u = 0; u < kMoves; ++u) {
-    if (src[u] < 0) continue;
     const int64_t j = j0 + 4 * u;
+    if (src[u] < 0 || !in_bounds(j, 1, a.dst_cap, a.err)) continue;
     uint8_t* blk = a.dst + kv4_block_offset(bh, a.dst_cap, j);
     const int at = static_cast<int>(j % kKv4BlockSlots);
     *reinterpret_cast<int4*>(blk + c_at + at * 64) = codes[u];
     if (part == 0) *reinterpret_cast<int4*>(blk + kKv4MetaOffset + at * 16) = meta[u];
-    if (part == 1) a.dst_weight[bh * a.dst_cap + j] = __int_as_float(word[u]);
-    if (part == 2) dpos[j] = word[u];
+    if (part == 1) store_at(a.dst_weight, to + j, dst_slots, __int_as_float(word[u]), a.err);
+    if (part == 2) store_at(a.dst_pos, to + j, dst_slots, word[u], a.err);
   }
 }
 
