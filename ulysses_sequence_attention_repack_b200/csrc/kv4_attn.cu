@@ -1281,7 +1281,9 @@ cudaError_t launch_kv4_attn(const Kv4AttnLaunch& p, cudaStream_t stream) {
       p.weight ? static_cast<int64_t>(p.B) * p.H * ((p.cap + kWeightSlots - 1) / kWeightSlots) : 0;
   // a warp a row where there are more rows than blocks fit the GPU at once (1,344 rows of a ragged batch: 8 us with a
   // block each, 5 with a warp); fewer rows were cut into more parts each
-  const int per_block = rows > 4 * 148 ? kJoinWarps : 1;
+  int dev = 0, sms = 1;
+  if ((e = current_device_sms(&dev, &sms)) != cudaSuccess) return e;
+  const int per_block = rows > 4 * sms ? kJoinWarps : 1;
   const int64_t row_blocks = (rows + per_block - 1) / per_block;
   if (row_blocks + weight_blocks > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_after(rpb == 8 ? kv4_join_kernel<8> : kv4_join_kernel<16>,

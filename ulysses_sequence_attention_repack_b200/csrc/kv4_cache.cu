@@ -617,17 +617,17 @@ cudaError_t launch_kv4_evict(const Kv4EvictLaunch& a, cudaStream_t stream) {
   // blocks an SM: 56 pairs of 104,448 slots take 5 each; 8 took two rounds and
   // half as long again), but 4,096 slots each at least.  A block holds its keys
   // where two blocks' fit an SM, else makes them anew each time.
-  int dev = 0;
-  int cluster = std::max(1, std::min(kMaxCluster, 2 * 148 / pairs));
+  int dev = 0, sms = 1;
+  cudaError_t e = current_device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  int cluster = std::max(1, std::min(kMaxCluster, 2 * sms / pairs));
   cluster = static_cast<int>(std::min<int64_t>(cluster, (a.src_cap + 4095) / 4096));
   const int64_t run = (a.src_cap + 4 * cluster - 1) / (4 * cluster) * 4;
   const bool held = run <= kHeldKeys;
   static PerDeviceOnce once;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess)
-    e = once.run(dev, [] {
-      return cudaFuncSetAttribute(kv4_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
-    });
+  e = once.run(dev, [] {
+    return cudaFuncSetAttribute(kv4_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
+  });
   if (e != cudaSuccess) return e;
   e = launch_after(held ? kv4_select_kernel<true> : kv4_select_kernel<false>,
                    dim3(static_cast<unsigned>(pairs) * cluster), kSelThreads, held ? run * 4 : 0, cluster, stream, a,
