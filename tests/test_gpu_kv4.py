@@ -1135,3 +1135,29 @@ def test_small_query_values_keep_their_bits(gpu, q_len, G):
     k[..., 64:] *= 2.0 ** 28
     U.ulysses_kv4_append(kv, cache, k, v, _i32([0, n], gpu), _i32([0], gpu))
     _attend(gpu, kv, cache, q, [n], True)
+
+
+def test_a_load_of_many_tokens_equals_loads_of_few(gpu):
+    """Ragged sequences at odd slots in one call, which takes runs of tokens, against a call a sequence, which takes
+    one at a time; two heads against the held values."""
+    import torch
+    heads, lens, start = 56, [40, 0, 7, 1, 5, 60, 3], [3, 0, 31, 95, 30, 33, 64]
+    B = len(lens)
+    kv, cache, _, _ = _make(gpu, [96] * B, heads, 96, 160)
+    host = _host(kv, cache)
+    n = sum(lens)
+    k = torch.full((n + 2, heads, D), 9.0, dtype=torch.bfloat16, device=gpu)
+    v = torch.full_like(k, 9.0)
+    U.ulysses_kv4_load(kv, cache, k, v, _i32(_cu(lens), gpu), _i32(start, gpu))
+    one_k, one_v = torch.full_like(k, 9.0), torch.full_like(k, 9.0)
+    at = 0
+    for b, m in enumerate(lens):
+        cu = [0] * (b + 1) + [m] * (B - b)
+        U.ulysses_kv4_load(kv, cache, one_k[at:at + m], one_v[at:at + m], _i32(cu, gpu), _i32(start, gpu))
+        for h in (0, heads - 1):
+            for plane, got in ((0, k), (1, v)):
+                want, _ = host.values(b, h, start[b], start[b] + m, plane)
+                assert np.array_equal(_bits(got[at:at + m, h]), orc.f64_to_bf16(want))
+        at += m
+    assert torch.equal(k, one_k) and torch.equal(v, one_v)
+    assert bool((k[n:] == 9).all()) and U.ulysses_kv4_last_device_error(kv) == 0

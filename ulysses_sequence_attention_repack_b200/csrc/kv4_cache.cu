@@ -599,9 +599,15 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4EvictLaun
 
 cudaError_t launch_kv4_rows(bool load, Kv4RowsLaunch a, cudaStream_t stream) {
   if (a.r.rows == 0) return cudaSuccess;
-  // The load takes runs of tokens where sequences bring enough of them, and a
-  // warp a token where they bring one or a few, which a run would take one by one.
-  const bool runs = !load || a.r.rows >= static_cast<int64_t>(4 * kRun) * a.B;
+  // The load takes runs of tokens where sequences bring enough of them to fill
+  // runs and the launch enough of those to fill the GPU, else a warp a token
+  // (a run that crosses sequences goes one by one, and few runs are a longer
+  // wait than more warps).  Tokens a sequence x sequences x heads, us a token
+  // at a time / in runs: 4 x 256 x 8 3.7 / 4.7, 8 x 48 x 8 2.8 / 3.1, 16 x 48 x 8
+  // 3.6 / 3.3, 8 x 256 x 8 5.3 / 4.9, 16 x 48 x 56 11.5 / 8.0, 32 x 1024 x 8
+  // 72 / 32; 128 x 1 x 8 2.1 / 2.9, 64 x 1 x 56 3.1 / 3.0.
+  const bool runs =
+      !load || (a.r.rows >= static_cast<int64_t>(kRun) * a.B && a.r.rows * a.H >= 4096);
   const int64_t items = runs ? (a.r.rows + kRun - 1) / kRun * a.H : a.r.rows * a.H;
   const int64_t grid = (items + kWarps - 1) / kWarps;
   if (grid * kWarps > 0xffffffffll || grid > 0x7fffffff) return cudaErrorInvalidValue;
