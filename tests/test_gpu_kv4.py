@@ -1161,3 +1161,23 @@ def test_a_load_of_many_tokens_equals_loads_of_few(gpu):
         at += m
     assert torch.equal(k, one_k) and torch.equal(v, one_v)
     assert bool((k[n:] == 9).all()) and U.ulysses_kv4_last_device_error(kv) == 0
+
+
+@pytest.mark.parametrize("q_len,G", SHAPES)
+@pytest.mark.parametrize("kind", ["within", "beyond", "zeros"])
+def test_steps_of_one_block_that_differ(gpu, q_len, G, kind):
+    """The first power of two by the block's least step (steps within 2^8 of each other) and by each row's largest
+    p s (beyond that, and beside rows of one value, whose step is 0), for rows that look at different slots."""
+    import torch
+    n = 61
+    kv, cache, k, v = _make(gpu, [n], 2, 64, 170)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(171)
+    wide = torch.rand((n, 2, 1), generator=g, device=gpu) * {"within": 7.0, "beyond": 24.0, "zeros": 3.0}[kind]
+    v = (v * torch.exp2(wide)).to(torch.bfloat16)
+    if kind == "zeros":
+        v[::3, :, :64] = v[::3, :, :1]
+        v[1::5, :, 64:] = 0
+    q = _queries(gpu, 1, q_len, 2 * G, 172) * 4              # sharp: a row's weight sits on a few slots
+    U.ulysses_kv4_append(kv, cache, k, v, _i32([0, n], gpu), _i32([0], gpu))
+    _attend(gpu, kv, cache, q, [n], True, True)

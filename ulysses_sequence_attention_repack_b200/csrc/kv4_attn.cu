@@ -506,8 +506,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
     float acc[NT][8][4];
     float M[NT][2], Ms[NT][2], l[NT][2];   // Ms: M, or 0 while M is -inf
     float2 z0[NT][2], u[NT][2];            // of both groups: sums of p m, the rows' factors of p s
-    // a step that takes no row's p s past its bound, whatever p is: 2^(c + 2) of the least c
-    float s_limit[2] = {pow2(kLeastExp + 2), pow2(kLeastExp + 2)};
+    // a step that takes no row's p s past its bound, whatever p is: 2^(c + 2) of the least c of the rows with a maximum
+    // (infinity before any has one: a row's first slot moves its own)
+    float s_limit[2] = {INFINITY, INFINITY};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -762,7 +763,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
           }
       }
       if (__any_sync(0xffffffffu, move)) {
-        float up[2] = {pow2(kHeadroom - kMostExp), pow2(kHeadroom - kMostExp)};   // largest factor of a row with slots
+        // Where the block's steps are within 2^8 of each other, the least of them stands for the largest p s of a row whose
+        // maximum it moves (p is 1 there); else every row finds its own.
+        uint32_t least[2];
+        bool own = big;
+        {
+          const float4 mine = kput[32 + lane];
+          const float vs[2] = {fmaxf(mine.x, 0.f), fmaxf(mine.y, 0.f)};   // (what is no number takes no part)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t step = __float_as_uint(vs[w]);
+            least[w] = __reduce_min_sync(0xffffffffu, kEdge && slot0 + lane >= highest ? 0x7f800000u : step);
+            own |= (__reduce_max_sync(0xffffffffu, step) >> 23) >= (least[w] >> 23) + 8 || least[w] == 0;
+          }
+        }
+        float f[NT][2], y[NT][2][2];   // what the moves make of sums so far; the rows' largest p s
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -772,41 +787,72 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_attn_kernel(con
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
             const float m_new = m > M[nt][c] + kGrow ? m : M[nt][c];
-            const float f = m_new == M[nt][c] ? 1.f : ex2(M[nt][c] - m_new);
+            f[nt][c] = m_new == M[nt][c] ? 1.f : ex2(M[nt][c] - m_new);
             M[nt][c] = m_new;
             Ms[nt][c] = m_new == NEG_INF ? 0.f : m_new;
-            l[nt][c] *= f;
-            z0[nt][c].x *= f;
-            z0[nt][c].y *= f;
-            float y[2] = {0.f, 0.f};   // the row's largest p s (what is no number takes no part)
+            l[nt][c] *= f[nt][c];
+            z0[nt][c].x *= f[nt][c];
+            z0[nt][c].y *= f[nt][c];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float4 v = kput[32 + 8 * k + g];
-              float p = ex2(fmaf(s[nt][k >> 1][2 * (k & 1) + c], qscale[nt][c], -Ms[nt][c]));
-              if (kEdge && slot0 + 8 * k + g >= limit[nt][c]) p = 0.f;
-              y[0] = fmaxf(y[0], p * v.x);
-              y[1] = fmaxf(y[1], p * v.y);
-            }
-            // both groups' in one word: their leading halves, whose order is theirs
-            uint32_t both = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632u);
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, d));
-            const float down0 = move_power(u[nt][c].x, f, bf16_lo(both)), down1 = move_power(u[nt][c].y, f, bf16_hi(both));
-            if (m_new != NEG_INF) {
-              up[0] = fmaxf(up[0], u[nt][c].x);
-              up[1] = fmaxf(up[1], u[nt][c].y);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              acc[nt][i][c] *= i < 4 ? down0 : down1;
-              acc[nt][i][c + 2] *= i < 4 ? down0 : down1;
-            }
+            for (int w = 0; w < 2; ++w) y[nt][c][w] = f[nt][c] != 1.f ? __uint_as_float(least[w]) : 0.f;
           }
+        if (own) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          up[w] = fmaxf(up[w], __shfl_xor_sync(0xffffffffu, up[w], 1));
-          up[w] = fmaxf(up[w], __shfl_xor_sync(0xffffffffu, up[w], 2));
-          s_limit[w] = pow2(kHeadroom + 2 - exponent(up[w]));
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float4 v = kput[32 + 8 * k + g];
+                float p = ex2(fmaf(s[nt][k >> 1][2 * (k & 1) + c], qscale[nt][c], -Ms[nt][c]));
+                if (kEdge && slot0 + 8 * k + g >= limit[nt][c]) p = 0.f;
+                y0 = fmaxf(y0, p * v.x);
+                y1 = fmaxf(y1, p * v.y);
+              }
+              // both groups' in one word: their leading halves, whose order is theirs
+              uint32_t both = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632u);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, d));
+              y[nt][c][0] = bf16_lo(both);
+              y[nt][c][1] = bf16_hi(both);
+            }
+        }
+        if (s_limit[0] == INFINITY && !own) {
+          // nothing is summed yet, and all rows get one power: most fragments' first block (5 ragged sequences of 14 x 2
+          // heads, 8 tokens: 55.4 us the long way, 54.2 so)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int e = max(kLeastExp, min(kMostExp, exponent(__uint_as_float(least[w]))));
+            s_limit[w] = pow2(e + 2);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) (w ? u[nt][c].y : u[nt][c].x) = pow2(kHeadroom - e);
+          }
+        } else {
+          float up[2] = {pow2(kHeadroom - kMostExp), pow2(kHeadroom - kMostExp)};   // largest factor of a row with slots
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float down0 = move_power(u[nt][c].x, f[nt][c], y[nt][c][0]);
+              const float down1 = move_power(u[nt][c].y, f[nt][c], y[nt][c][1]);
+              if (M[nt][c] != NEG_INF) {
+                up[0] = fmaxf(up[0], u[nt][c].x);
+                up[1] = fmaxf(up[1], u[nt][c].y);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                acc[nt][i][c] *= i < 4 ? down0 : down1;
+                acc[nt][i][c + 2] *= i < 4 ? down0 : down1;
+              }
+            }
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(up[w]));
+            s_limit[w] = pow2(kHeadroom + 2 - exponent(__uint_as_float(most)));
+          }
         }
       }
       // p, its sums, and p s as the operand of the second product
