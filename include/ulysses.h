@@ -576,8 +576,9 @@ int ulysses_kv4_append(const ulysses_kv4_t* kv, void* cache, const void* k, cons
                        const int32_t* dev_cu, const int32_t* dev_start, const int32_t* dev_pos0, void* stream);
 
 /*
- * The way back: K and V rows as bf16(m + s n), laid out as the append's (for
- * the attention of a long chunk over its cached prefix by ulysses_attn_fwd).
+ * The way back: K and V rows as bf16(m + s n), laid out as the append's, for
+ * whatever wants plain rows.  (ulysses_attn_fwd takes Q, K and V of one length:
+ * queries behind a cached prefix go through ulysses_kv4_attn.)
  * Rows outside every sequence stay as they are.  Destination rows must not
  * share elements.  Errors: as ulysses_kv4_append.
  */
@@ -625,8 +626,11 @@ int ulysses_kv4_attn(const ulysses_kv4_t* kv, void* cache, const void* q, int32_
  * number).  The kept slots move, in their order, into slots 0 on of the
  * destination cache (same batch and heads, capacity >= keep) with their
  * weights and positions; its further slots stay as they are.  A sequence of at
- * most `keep` slots moves whole.  dev_new_lengths[b] = min(dev_lengths[b],
- * keep).  The caches must not overlap, nor the two length arrays.
+ * most `keep` slots moves whole.  Appended slots have weight 0 until an
+ * attention with ULYSSES_KV4_WEIGHTS has looked at them: to cut a cache down
+ * right after its prompt, run the prompt's last queries (16, say, causal) with
+ * the flag first, or the slots between are kept from the lowest.
+ * dev_new_lengths[b] = min(dev_lengths[b], keep).  The caches must not overlap, nor the two length arrays.
  * Errors: ARG, ALIGN, CUDA.
  */
 int ulysses_kv4_evict(const ulysses_kv4_t* src_kv, const void* src_cache, const ulysses_kv4_t* dst_kv, void* dst_cache,

@@ -45,11 +45,13 @@
 // Measured (one B200, device time): 104,448 slots x 56 heads, one query row,
 // 842 MB: 140 us (6.0 TB/s of 6.55 measured) at 1.95 GHz, 158 us in a loop of
 // half a second, where the 1000 W cap holds 1.76 GHz; its copies alone take 125.
-// Memory and the ALU share the time: of 382 instructions a warp spends on a
+// Memory and the ALU share the time: of 384 instructions a warp spends on a
 // block, 176 are the ANDs, shifts and byte moves that make operands of codes,
-// and the ALU runs at half rate.  With 8 rows 500 instructions a block bound it
-// (8 heads x 313,344 slots: 77 us, 4.7 TB/s), with 16 rows the dependences of
-// two warps a scheduler (14 heads x 104,448: 72 us, 2.9 TB/s).
+// and the ALU, at half rate, is 58% busy.  With more rows neither is the bound:
+// with 8 (495 instructions a block, 8 heads x 313,344 slots: 79 us, 4.5 TB/s)
+// issue slots and ALU are half busy and each warp waits on its own results, three
+// warps a scheduler; with 16 (662, two warps a scheduler, 14 heads x 104,448: 73
+// us, 2.9 TB/s) issue slots are 43% busy and the ALU 36%.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
